@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(OUT_DIR, "libgdrbwd.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "k0_chunk_indices.cu", "k1_wy_prep.cu", "k2_scan_tc.cu", "k3_scan_tc.cu", "k23_combine.cu",
            "k4_intra_grad.cu", "k4_intra_grad_tc.cu", "k5_dg_reduce.cu", "k7_wy_inputs.cu", "k8_qr.cu",
-           "noalloc.cu"]
+           "noalloc.cu", "block_api.cu", "k9_norms.cu", "k9_norms_f32.cu", "k9_norms_bf16.cu", "k9_norms_f16.cu",
+           "k10_linrec.cu", "k11_clip.cu"]
 
 
 def nvcc() -> str:
@@ -31,7 +32,8 @@ def nvcc() -> str:
 
 def _deps_mtime() -> float:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(os.path.dirname(HERE), "include", "gdr_bwd.h"))
+    inc = os.path.join(os.path.dirname(HERE), "include")
+    files += [os.path.join(inc, f) for f in ("gdr_bwd.h", "gdr_block.h")]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 

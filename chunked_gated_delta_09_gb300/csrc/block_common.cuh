@@ -1,0 +1,112 @@
+// block_common.cuh -- device-side pieces of the operators around the delta rule (include/gdr_block.h) and the
+// host-side launchers that block_api.cu calls.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gdr_common.cuh"
+#include "gdr_kernels.h"
+
+namespace gdr {
+
+// N consecutive elements moved as one access (two when they exceed 16 bytes).
+template <typename T, int N> struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
+    T v[N];
+};
+template <typename T, int N> __device__ __forceinline__ Pack<T, N> load_pack(const T *p) {
+    return *reinterpret_cast<const Pack<T, N> *>(p);
+}
+template <typename T, int N> __device__ __forceinline__ void unpack(const Pack<T, N> &a, float (&o)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = to_f32(a.v[i]);
+}
+template <typename T, int N> __device__ __forceinline__ void store_pack(T *p, const float (&x)[N]) {
+    Pack<T, N> a;
+#pragma unroll
+    for (int i = 0; i < N; ++i) a.v[i] = to_out_t<T>(x[i]);
+    *reinterpret_cast<Pack<T, N> *>(p) = a;
+}
+
+// n / d for n < 2^31 by one multiplication: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d) the error
+// m d - 2^(31 + s) is below d <= 2^s, so n m / 2^(31 + s) exceeds n / d by less than 1 / d.
+struct FastDiv {
+    uint32_t d, m, s;
+    static FastDiv of(uint32_t d) {
+        uint32_t s = 0;
+        while ((1ull << s) < d) ++s;
+        return {d, (uint32_t)(((1ull << (31 + s)) + d - 1) / d), 31 + s};
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (uint32_t)(((uint64_t)n * m) >> s); }
+};
+
+// Where row (token, head) of a strided tensor starts, rows counted token by token.
+struct RowMap {
+    int64_t ts, hs;
+    __device__ __forceinline__ int64_t at(uint32_t row, const FastDiv &heads) const {
+        if (heads.d == 1) return (int64_t)row * ts;
+        const uint32_t t = heads.div(row);
+        return (int64_t)t * ts + (int64_t)(row - t * heads.d) * hs;
+    }
+};
+
+struct GatedNormParams {
+    const void *dy, *x, *z, *weight;
+    void *y, *dx, *dz, *dweight;
+    float *part;  // backward: [CTAs][dim] column sums
+    RowMap dym, xm, zm;
+    FastDiv heads;
+    uint32_t rows;
+    int dim, dtype, weight_dtype, act;
+    float eps;
+    bool vec;  // rows are moved in 16-byte pieces
+};
+
+struct AddNormParams {
+    const void *dy, *dres, *x, *residual, *weight, *scale_vec;
+    void *y, *residual_out, *dx, *dresidual, *dweight, *dscale;
+    float *part;  // backward: [CTAs][1 or 2][dim] column sums
+    int64_t dy_ts, dres_ts, x_ts, r_ts, ro_ts;
+    uint32_t rows;
+    int dim, dtype, residual_dtype, weight_dtype, scale_dtype;
+    float scale, eps;
+    bool vec;
+};
+
+struct LinrecParams {
+    const void *x, *g, *dh;
+    const float *h0, *dht;
+    const int32_t *cu;
+    void *h, *dx, *dg;
+    float *ht, *dh0, *states;
+    int64_t x_ts, g_ts, dh_ts;
+    int rows, tokens, dim, N, complement;  // rows = batch * tokens; N sequences
+    int dtype, gate_dtype;
+    bool vec;
+    int *status;
+    uint32_t spin;
+};
+
+struct StepParams {
+    const void *x, *g;
+    const int32_t *slots;
+    float *state;
+    void *y;
+    int64_t x_ts, g_ts, batch, num_slots;
+    int dim, dtype, gate_dtype, complement;
+    bool vec;
+};
+
+// CTAs that write partial column sums, at most (the workspace is sized for it).
+constexpr int NORM_MAX_PARTS = 152 * 8;
+int norm_parts(int64_t rows, int64_t dim);
+
+cudaError_t launch_gated_norm_fwd(const GatedNormParams &p, cudaStream_t stream);
+cudaError_t launch_gated_norm_bwd(const GatedNormParams &p, cudaStream_t stream);
+cudaError_t launch_add_norm_fwd(const AddNormParams &p, cudaStream_t stream);
+cudaError_t launch_add_norm_bwd(const AddNormParams &p, cudaStream_t stream);
+cudaError_t launch_linrec_fwd(const LinrecParams &p, cudaStream_t stream);
+cudaError_t launch_linrec_bwd(const LinrecParams &p, cudaStream_t stream);
+cudaError_t launch_linrec_step(const StepParams &p, cudaStream_t stream);
+
+}  // namespace gdr

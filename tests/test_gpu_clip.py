@@ -1,0 +1,114 @@
+"""The gradient norm and clip on the GPU against 64 bits: mixed types and sizes, empty tensors, odd alignment, more
+tensors than one launch holds, norms that are zero or not finite, in place and into other types."""
+import pytest
+import torch
+
+import block_util as U
+from chunked_gated_delta_09_gb300 import clip_grad_norm, grad_norm
+
+pytestmark = pytest.mark.gpu
+
+
+def norm64(ts):
+    return float(sum(U.f64(t).square().sum() for t in ts)) ** 0.5
+
+
+def check(grads, max_norm, out=None, eps=1e-6):
+    ref = [U.f64(t) for t in grads]
+    n = norm64(grads)
+    assert abs(float(grad_norm(grads)) - n) <= U.FP32_BAR * n
+    got = clip_grad_norm(grads, max_norm, out, eps=eps)
+    assert got.shape == () and got.dtype == torch.float32 and abs(float(got) - n) <= U.FP32_BAR * n
+    f = min(1.0, max_norm / (n + eps))
+    for t, r in zip(grads if out is None else out, ref):
+        if t.numel():
+            assert U.rel(t, f * r) <= U.BAR[t.dtype]
+    if out is not None:
+        assert all(torch.equal(U.f64(t), r) for t, r in zip(grads, ref))
+
+
+SHAPES = [(64, 64), (1,), (0,), (7, 13), (33000,), (3, 0, 5), (16384,), (16385,), (128,)]
+
+
+@pytest.mark.parametrize("max_norm", [0.5, 1e6])
+@pytest.mark.parametrize("where", ["in place", "f32", "bf16"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_clip(dtype, where, max_norm):
+    gen = U.seeded(1)
+    grads = [U.randn(gen, *s, dtype=dtype) for s in SHAPES]
+    out = None
+    if where != "in place":
+        out = [torch.full_like(t, float("nan"), dtype=torch.float32 if where == "f32" else torch.bfloat16) for t in grads]
+    check(grads, max_norm, out)
+
+
+def test_mixed_types_and_odd_alignment():
+    gen = U.seeded(2)
+    grads = [U.randn(gen, 1001, dtype=torch.bfloat16)[1:], U.randn(gen, 70000)[3:], U.randn(gen, 9, dtype=torch.float16),
+             U.randn(gen, 40000, dtype=torch.bfloat16)[8:]]
+    check(grads, 1.0, [torch.empty(t.numel() + 1, device="cuda")[1:] for t in grads])
+    check(grads, 1.0)
+
+
+@pytest.mark.parametrize("count", [1, 639, 640, 641, 1500])
+def test_many_tensors(count):
+    gen = U.seeded(count)
+    flat = U.randn(gen, count * 40)
+    grads = [flat[40 * i:40 * i + 1 + i % 39] for i in range(count)]
+    check(grads, 1.0)
+
+
+def test_large_total():
+    """More elements than the grid takes in one round."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    grads = [torch.randn(n, generator=gen, device="cuda").bfloat16() for n in (30_000_001, 5, 12_000_000)]
+    n = float(torch.stack([t.double().square().sum() for t in grads]).sum().sqrt())
+    out = [torch.empty_like(t, dtype=torch.float32) for t in grads]
+    got = clip_grad_norm(grads, 10.0, out)
+    assert abs(float(got) - n) <= U.FP32_BAR * n
+    for t, o in zip(grads, out):
+        assert float((o.double() - t.double() * (10.0 / (n + 1e-6))).norm() / o.double().norm()) <= U.FP32_BAR
+
+
+def test_norms_that_are_zero_or_not_finite():
+    z = [torch.zeros(100, device="cuda"), torch.zeros(0, device="cuda")]
+    assert float(clip_grad_norm(z, 1.0)) == 0.0 and not z[0].any()
+    assert float(grad_norm([torch.zeros(0, device="cuda")])) == 0.0
+    assert float(clip_grad_norm([torch.zeros(0, device="cuda")], 1.0)) == 0.0
+    g = [torch.tensor([1.0, float("inf"), -2.0], device="cuda"), torch.ones(5, device="cuda")]
+    assert float(clip_grad_norm(g, 1.0)) == float("inf")
+    assert torch.equal(g[1], torch.zeros_like(g[1])) and torch.isnan(g[0][1]) and g[0][0] == 0
+    g = [torch.tensor([1.0, float("nan")], device="cuda"), torch.ones(5, device="cuda")]
+    assert torch.isnan(clip_grad_norm(g, 1.0)) and torch.isnan(g[1]).all()
+    g = [torch.ones(4, device="cuda")]
+    assert float(clip_grad_norm(g, 0.0)) == 2.0 and not g[0].any()
+
+
+def test_results_repeat_bit_for_bit_and_streams():
+    gen = U.seeded(4)
+    grads = [U.randn(gen, 200001), U.randn(gen, 77)]
+    a = clip_grad_norm(grads, 1.0, [torch.empty_like(t) for t in grads])
+    assert all(torch.equal(a, grad_norm(grads)) for _ in range(5))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    b = clip_grad_norm(grads, 1.0, [torch.empty_like(t) for t in grads], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(a, b)
+
+
+def test_capture_in_a_graph():
+    """The call copies nothing from the host, so a training step that ends with it can be captured."""
+    gen = U.seeded(5)
+    grads = [U.randn(gen, 5000), U.randn(gen, 300, dtype=torch.bfloat16)]
+    out = [torch.empty_like(t, dtype=torch.float32) for t in grads]
+    clip_grad_norm(grads, 1.0, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm = clip_grad_norm(grads, 1.0, out)
+    for t in grads:
+        t.mul_(3.0)
+    graph.replay()
+    n = norm64(grads)
+    assert abs(float(norm) - n) <= U.FP32_BAR * n
+    assert all(U.rel(o, U.f64(t) / (n + 1e-6)) <= U.FP32_BAR for o, t in zip(out, grads))

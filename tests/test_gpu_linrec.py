@@ -1,0 +1,192 @@
+"""The gated linear recurrence on the GPU against the token-by-token 64-bit form: dense and packed sequences, lengths of
+zero and one, odd sizes and strides, its backward with and without saved states, its single-token step."""
+import pytest
+import torch
+
+import block_util as U
+from chunked_gated_delta_09_gb300 import GdrError, _lib, linear_recurrence, linrec_bwd, linrec_fwd, linrec_step
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def problem(B, T, D, dtype, gtype, seed, lens=None):
+    gen = U.seeded(seed)
+    dt, gt = TYPES[dtype], TYPES[gtype]
+    N = B if lens is None else len(lens)
+    cu = None
+    if lens is not None:
+        cu = torch.tensor([sum(lens[:i]) for i in range(N + 1)], dtype=torch.int32, device="cuda")
+    return dict(x=U.randn(gen, B, T, D, dtype=dt), g=U.gates(gen, B, T, D, dtype=gt), h0=U.randn(gen, N, D),
+                cu_seqlens=cu), dict(dh=U.randn(gen, B, T, D, dtype=dt), dht=U.randn(gen, N, D))
+
+
+def check(p, d, lens, complement):
+    h, ht, states = linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"], complement=complement, return_states=True,
+                               check_status=True)
+    got = dict(h=h, ht=ht)
+    got.update(linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], p["cu_seqlens"], states, complement=complement,
+                          check_status=True))
+    U.check(got, U.linrec(p["x"], p["g"], p["h0"], lens, complement, d["dh"], d["dht"]))
+    return got
+
+
+@pytest.mark.parametrize("complement", [False, True], ids=["plain", "complement"])
+@pytest.mark.parametrize("dtype,gtype", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"), ("f16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("B,T,D", [(1, 1, 1), (3, 1, 40), (2, 7, 33), (1, 64, 128), (2, 65, 130), (3, 200, 8),
+                                   (1, 300, 256), (5, 63, 31)])
+def test_dense(B, T, D, dtype, gtype, complement):
+    p, d = problem(B, T, D, dtype, gtype, seed=B + T + D)
+    check(p, d, None, complement)
+
+
+@pytest.mark.parametrize("D", [64, 37])
+@pytest.mark.parametrize("lens", [[5], [0, 3, 0, 0, 130, 1, 1, 64, 0], [64, 64, 64], [1] * 70, [63, 65, 1, 127, 200],
+                                  [0, 0, 9], [2000, 3, 900]], ids=str)
+def test_packed(lens, D):
+    p, d = problem(1, sum(lens), D, "bf16", "f32", seed=len(lens) + D, lens=lens)
+    check(p, d, lens, True)
+
+
+@pytest.mark.parametrize("T,D", [(20000, 32), (5000, 200)])
+def test_long_sequences(T, D):
+    """Enough rows that a state passes through many tiles."""
+    p, d = problem(1, T, D, "f32", "f32", seed=T)
+    check(p, d, None, False)
+
+
+def test_no_tokens():
+    p, d = problem(2, 0, 8, "f32", "f32", seed=1)
+    h, ht = linrec_fwd(p["x"], p["g"], p["h0"])
+    assert h.shape == (2, 0, 8) and torch.equal(ht, p["h0"])
+    got = linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"])
+    assert torch.equal(got["dh0"], d["dht"])
+    p, d = problem(1, 0, 8, "f32", "f32", seed=1, lens=[0, 0])
+    h, ht = linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"], check_status=True)
+    assert torch.equal(ht, p["h0"])
+
+
+def test_absent_states_and_backward_without_saved_states():
+    p, d = problem(1, 400, 48, "bf16", "f32", seed=2, lens=[150, 0, 250])
+    p["h0"] = None
+    d["dht"] = None
+    got = check(p, d, [150, 0, 250], True)
+    again = linrec_bwd(p["x"], p["g"], d["dh"], None, None, p["cu_seqlens"], complement=True)
+    assert all(torch.equal(got[k], again[k]) for k in again)
+
+
+def test_strided_rows():
+    gen = U.seeded(5)
+    for pad in (8, 3):
+        wide = U.randn(gen, 2, 90, 3 * 64 + pad, dtype=torch.bfloat16)
+        x, dh = wide[..., :64], wide[..., 64:128]
+        g = U.gates(gen, 2, 90, 128, dtype=torch.bfloat16)[..., 5:69]
+        p = dict(x=x, g=g, h0=U.randn(gen, 2, 64), cu_seqlens=None)
+        check(p, dict(dh=dh, dht=U.randn(gen, 2, 64)), None, True)
+
+
+def test_a_gate_of_zero_and_a_nan_stay_in_their_place():
+    """a = 0 (g = -inf) forgets the past; a nan reaches the rest of its own sequence and no other one."""
+    lens = [100, 90, 80]
+    p, d = problem(1, 270, 36, "f32", "f32", seed=6, lens=lens)
+    p["g"][0, 50] = float("-inf")
+    p["g"][0, 129, 3] = float("-inf")
+    p["g"][0, 200] = 0.0
+    check(p, d, lens, True)
+    clean, _ = linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"])
+    p["x"][0, 110, 7] = float("nan")
+    h, ht, states = linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"], return_states=True)
+    bad = torch.isnan(h)
+    assert bad[0, 110:190, 7].all() and bad.sum() == 80
+    assert torch.equal(h[~bad], clean[~bad]) and torch.isnan(ht).sum() == 1
+    d["dh"][0, 195, 2] = float("inf")
+    got = linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], p["cu_seqlens"], states)
+    assert torch.isfinite(got["dx"][0, :190]).all() and torch.isfinite(got["dx"][0, 196:]).all()
+
+
+def test_results_repeat_bit_for_bit():
+    p, d = problem(1, 9000, 96, "bf16", "f32", seed=7)
+    first = None
+    for _ in range(5):
+        h, ht, states = linrec_fwd(p["x"], p["g"], p["h0"], return_states=True)
+        got = linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], None, states)
+        now = [h, ht, *got.values()]
+        first = first or now
+        assert all(torch.equal(a, b) for a, b in zip(first, now))
+
+
+@pytest.mark.parametrize("cu", [[0, 100, 60, 201], [1, 50, 100, 201], [0, 50, 100, 200], [0, 50, 300, 201],
+                                [0, -5, 100, 201]], ids=str)
+def test_malformed_cu_seqlens_are_reported(cu):
+    p, d = problem(1, 201, 40, "f32", "f32", seed=8, lens=[100, 50, 51])
+    _, _, states = linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"], return_states=True, check_status=True)
+    bad = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    with pytest.raises(GdrError) as e:
+        linrec_fwd(p["x"], p["g"], p["h0"], bad, check_status=True)
+    assert e.value.status == _lib.GDR_ERR_DEVICE
+    with pytest.raises(GdrError) as e:
+        linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], bad, states, check_status=True)
+    assert e.value.status == _lib.GDR_ERR_DEVICE
+
+
+def test_autograd_and_differences():
+    p, _ = problem(1, 150, 20, "f32", "f32", seed=9, lens=[70, 1, 79])
+    leaves = {k: p[k].requires_grad_() for k in ("x", "g", "h0")}
+    h, ht = linear_recurrence(p["x"], p["g"], p["h0"], p["cu_seqlens"], complement=True)
+    (h.sum() + 2.0 * ht.sum()).backward()
+    gen = U.seeded(10)
+    for name, leaf in leaves.items():
+        d = torch.randn(leaf.shape, generator=gen, dtype=torch.float64)
+
+        def loss(step):
+            v = {k: U.f64(t) + (step * d if k == name else 0.0) for k, t in leaves.items()}
+            o = U.linrec(v["x"], v["g"], v["h0"], [70, 1, 79], True)
+            return float(o["h"].sum() + 2.0 * o["ht"].sum())
+
+        diff = (loss(1e-5) - loss(-1e-5)) / 2e-5
+        grad = U.f64(leaf.grad)
+        # truncation h^2 f''' / 6 with sums over up to 79 tokens: below 1e-6 of the gradient's size
+        assert abs(float((grad * d).sum()) - diff) <= 2 * U.FP32_BAR * float(grad.norm() * d.norm()), name
+
+
+# ---------------------------------------------------------------- single tokens
+@pytest.mark.parametrize("complement", [False, True], ids=["plain", "complement"])
+@pytest.mark.parametrize("dtype,gtype", [("f32", "f32"), ("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("B,D,pad", [(1, 1, 0), (3, 33, 0), (64, 2048, 0), (5, 64, 8), (7, 64, 3)])
+def test_step(B, D, pad, dtype, gtype, complement):
+    gen = U.seeded(B + D + pad)
+    x = U.randn(gen, B, D + pad, dtype=TYPES[dtype])[:, :D]
+    g = U.gates(gen, B, D + pad, dtype=TYPES[gtype])[:, :D]
+    state = U.randn(gen, B + 9, D)
+    slots = torch.randperm(B + 9, generator=gen)[:B].to(torch.int32).cuda()
+    if B > 2:
+        slots[1] = -1
+    if B > 4:
+        slots[3] = B + 9
+    ref, y_ref = U.f64(state), torch.zeros(B, D, dtype=torch.float64)
+    for i, s in enumerate(slots.tolist()):
+        if 0 <= s < B + 9:
+            a, rest = torch.exp(U.f64(g[i])), -torch.expm1(U.f64(g[i]))
+            ref[s] = y_ref[i] = a * ref[s] + (rest if complement else 1.0) * U.f64(x[i])
+    y = linrec_step(x, g, state, slots, complement=complement)
+    U.check(dict(y=y, state=state), dict(y=y_ref, state=ref))
+
+
+def test_steps_continue_a_prefill():
+    p, _ = problem(3, 40, 72, "bf16", "bf16", seed=11)
+    h, ht = linrec_fwd(p["x"], p["g"], p["h0"], complement=True)
+    _, state = linrec_fwd(p["x"][:, :30].contiguous(), p["g"][:, :30].contiguous(), p["h0"], complement=True)
+    for t in range(30, 40):
+        y = linrec_step(p["x"][:, t], p["g"][:, t], state, complement=True)
+        assert U.rel(y, U.f64(h[:, t])) <= 2 * U.BAR[torch.bfloat16]
+    assert U.rel(state, U.f64(ht)) <= U.FP32_BAR
+
+
+def test_step_of_nothing():
+    state = torch.ones(4, 16, device="cuda")
+    x = torch.empty(0, 16, device="cuda")
+    assert linrec_step(x, x, state).shape == (0, 16)
+    x = torch.ones(2, 16, device="cuda")
+    y = linrec_step(x, x, state, torch.tensor([-1, -1], dtype=torch.int32, device="cuda"))
+    assert not y.any() and torch.equal(state, torch.ones_like(state))
