@@ -20,7 +20,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "k0_chunk_indices.cu", "k1_wy_prep.cu", "k2_scan_tc.cu", "k3_scan_tc.cu", "k23_combine.cu",
            "k4_intra_grad.cu", "k4_intra_grad_tc.cu", "k5_dg_reduce.cu", "k7_wy_inputs.cu", "k8_qr.cu",
            "noalloc.cu", "block_api.cu", "k9_norms.cu", "k9_norms_f32.cu", "k9_norms_bf16.cu", "k9_norms_f16.cu",
-           "k10_linrec.cu", "k11_clip.cu"]
+           "k10_linrec.cu", "k10_linrec_f32.cu", "k10_linrec_bf16.cu", "k10_linrec_f16.cu", "k11_clip.cu"]
 
 
 def nvcc() -> str:

@@ -214,7 +214,7 @@ gdr_status gdr_add_norm_bwd(const gdr_add_norm_bwd_args *a, void *stream_) {
 // ---------------------------------------------------------------- gated linear recurrence
 size_t gdr_linrec_workspace_bytes(int64_t rows, int64_t dim) {
     if (rows < 0 || rows > kMaxRows || dim < 1) return 0;
-    return 256;
+    return linrec_workspace(rows, dim);
 }
 
 static gdr_status linrec_sizes(int64_t batch, int64_t tokens, int64_t dim, int64_t num_seqs, int dtype, int gate_dtype,
@@ -224,6 +224,8 @@ static gdr_status linrec_sizes(int64_t batch, int64_t tokens, int64_t dim, int64
         return GDR_ERR_INVALID_ARG;
     if (batch > kMaxRows || tokens > kMaxRows || batch * tokens > kMaxRows || dim > (1 << 20) || num_seqs > (1 << 24))
         return GDR_ERR_UNSUPPORTED;
+    // (tiles x blocks of 32 channels number the CTAs)
+    if ((batch * tokens / GDR_LINREC_TILE + 1) * ((dim + 31) / 32) >= (1ll << 31)) return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
 }
 
@@ -261,7 +263,6 @@ gdr_status gdr_linrec_fwd(const gdr_linrec_fwd_args *a, void *stream_) {
     p.dtype = a->dtype, p.gate_dtype = a->gate_dtype;
     p.vec = v.ok;
     p.status = (int *)a->workspace, p.spin = spin_limit();
-    if (cudaMemsetAsync(a->workspace, 0, 256, stream) != cudaSuccess) return GDR_ERR_CUDA;
     return done(launch_linrec_fwd(p, stream));
 }
 
@@ -300,7 +301,6 @@ gdr_status gdr_linrec_bwd(const gdr_linrec_bwd_args *a, void *stream_) {
     p.dtype = a->dtype, p.gate_dtype = a->gate_dtype;
     p.vec = v.ok;
     p.status = (int *)a->workspace, p.spin = spin_limit();
-    if (cudaMemsetAsync(a->workspace, 0, 256, stream) != cudaSuccess) return GDR_ERR_CUDA;
     return done(launch_linrec_bwd(p, stream));
 }
 
@@ -319,7 +319,8 @@ gdr_status gdr_linrec_step(const gdr_linrec_step_args *a, void *stream) {
     if (a->batch < 0 || a->dim < 1 || a->num_slots < 0 || !type_ok(a->dtype) ||
         (a->gate_dtype != a->dtype && a->gate_dtype != GDR_F32) || (a->complement != 0 && a->complement != 1))
         return GDR_ERR_INVALID_ARG;
-    if (a->batch > 65535 || a->dim > (1 << 20) || a->num_slots > 0x7fffffffll) return GDR_ERR_UNSUPPORTED;
+    if (a->dim > (1 << 20) || a->num_slots > 0x7fffffffll || a->batch > kMaxRows || a->batch * a->dim > kMaxRows)
+        return GDR_ERR_UNSUPPORTED;
     if (!a->slots && a->num_slots < a->batch) return GDR_ERR_INVALID_ARG;
     if (a->batch == 0) return GDR_OK;
     if (!a->x || !a->g || !a->y || (a->num_slots > 0 && !a->state)) return GDR_ERR_INVALID_ARG;

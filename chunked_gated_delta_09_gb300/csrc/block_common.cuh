@@ -73,6 +73,9 @@ struct AddNormParams {
     bool vec;
 };
 
+// Rows of a tile of the recurrence's scans; a state is saved for each.
+constexpr int LR_TILE = 64;
+
 struct LinrecParams {
     const void *x, *g, *dh;
     const float *h0, *dht;
@@ -82,9 +85,16 @@ struct LinrecParams {
     int64_t x_ts, g_ts, dh_ts;
     int rows, tokens, dim, N, complement;  // rows = batch * tokens; N sequences
     int dtype, gate_dtype;
-    bool vec;
-    int *status;
+    bool vec;   // rows are moved in pieces of several elements
+    bool walk;  // one CTA walks all tiles of its channels
     uint32_t spin;
+    // the workspace: a status word, the ticket, and the tree of maps (tiles, groups, blocks, spans)
+    int *status, *ticket;
+    int *flags[4];    // [record][block of channels]
+    float2 *recs[4];  // [record][dim]
+    int tiles, nblk;  // tiles of rows, blocks of channels
+    unsigned grid;
+    FastDiv blocks, per_seq;  // divide by nblk, by tokens
 };
 
 struct StepParams {
@@ -95,6 +105,7 @@ struct StepParams {
     int64_t x_ts, g_ts, batch, num_slots;
     int dim, dtype, gate_dtype, complement;
     bool vec;
+    FastDiv pieces;
 };
 
 // CTAs that write partial column sums, at most (the workspace is sized for it).
@@ -105,8 +116,10 @@ cudaError_t launch_gated_norm_fwd(const GatedNormParams &p, cudaStream_t stream)
 cudaError_t launch_gated_norm_bwd(const GatedNormParams &p, cudaStream_t stream);
 cudaError_t launch_add_norm_fwd(const AddNormParams &p, cudaStream_t stream);
 cudaError_t launch_add_norm_bwd(const AddNormParams &p, cudaStream_t stream);
-cudaError_t launch_linrec_fwd(const LinrecParams &p, cudaStream_t stream);
-cudaError_t launch_linrec_bwd(const LinrecParams &p, cudaStream_t stream);
-cudaError_t launch_linrec_step(const StepParams &p, cudaStream_t stream);
+size_t linrec_workspace(int64_t rows, int64_t dim);
+cudaError_t linrec_blocks(LinrecParams &p, int channels, cudaStream_t stream);
+cudaError_t launch_linrec_fwd(LinrecParams p, cudaStream_t stream);
+cudaError_t launch_linrec_bwd(LinrecParams p, cudaStream_t stream);
+cudaError_t launch_linrec_step(StepParams p, cudaStream_t stream);
 
 }  // namespace gdr

@@ -1,109 +1,90 @@
-// k10_linrec.cu -- the gated linear recurrence h_t = a_t h_{t-1} + b_t over packed or dense sequences, its backward
-// and its single-token step.
+// k10_linrec.cu -- the gated linear recurrence: workspace, grid, and choice by type.
 #include "block_common.cuh"
 
 namespace gdr {
+
+// A sequence of up to this many tiles is walked by one CTA per block of channels: a tile takes it about 2 us, and the
+// tree's cleared flags and hops cost more than that until there are as many.
+constexpr int LR_WALK = 4;
+
 namespace {
+size_t up(size_t n) { return (n + 255) & ~size_t(255); }
 
-constexpr int LR_TILE = 64;  // rows between saved states
-
-// a = exp(g) and, where the input is weighted by it, 1 - a.
-__device__ __forceinline__ void decay(float g, float &a, float &rest) {
-    const float e = expm1f(g);
-    a = g > -0.5f ? 1.f + e : expf(g);
-    rest = -e;
+// Records at each level of the tree over `tiles` tiles.
+void tree_sizes(int64_t tiles, int64_t (&n)[4]) {
+    for (int level = 0; level < 4; ++level) n[level] = (tiles + ((int64_t)1 << (3 * level)) - 1) >> (3 * level);
 }
-
-__device__ __forceinline__ void lr_range(const LinrecParams &p, int s, int &bos, int &eos) {
-    bos = p.cu ? p.cu[s] : s * p.tokens;
-    eos = p.cu ? p.cu[s + 1] : bos + p.tokens;
-    bos = max(0, min(bos, p.rows));
-    eos = max(bos, min(eos, p.rows));
-}
-
-// One thread walks one channel of one sequence.
-__global__ void k10_fwd(const LinrecParams p) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x, s = blockIdx.y;
-    if (p.cu && c == 0 && s == 0 && (p.cu[0] != 0 || p.cu[p.N] != p.rows)) atomicOr(p.status, ST_BAD_SEQLENS);
-    if (p.cu && c == 0 && p.cu[s + 1] < p.cu[s]) atomicOr(p.status, ST_BAD_SEQLENS);
-    if (c >= p.dim) return;
-    int bos, eos;
-    lr_range(p, s, bos, eos);
-    float h = p.h0 ? p.h0[(size_t)s * p.dim + c] : 0.f;
-    for (int t = bos; t < eos; ++t) {
-        float a, rest;
-        decay(load_scalar(p.g, (size_t)t * p.g_ts + c, p.gate_dtype), a, rest);
-        const float x = load_scalar(p.x, (size_t)t * p.x_ts + c, p.dtype);
-        if (p.states && t % LR_TILE == 0) p.states[(size_t)(t / LR_TILE) * p.dim + c] = h;
-        h = fmaf(a, h, p.complement ? rest * x : x);
-        if (p.h) store_scalar(p.h, (size_t)t * p.dim + c, h, p.dtype);
-    }
-    if (p.ht) p.ht[(size_t)s * p.dim + c] = h;
-}
-
-__global__ void k10_bwd(const LinrecParams p) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x, s = blockIdx.y;
-    if (p.cu && c == 0 && s == 0 && (p.cu[0] != 0 || p.cu[p.N] != p.rows)) atomicOr(p.status, ST_BAD_SEQLENS);
-    if (p.cu && c == 0 && p.cu[s + 1] < p.cu[s]) atomicOr(p.status, ST_BAD_SEQLENS);
-    if (c >= p.dim) return;
-    int bos, eos;
-    lr_range(p, s, bos, eos);
-    float mu = p.dht ? p.dht[(size_t)s * p.dim + c] : 0.f, before[LR_TILE];
-    for (int end = eos; end > bos;) {
-        const int start = max(bos, (end - 1) / LR_TILE * LR_TILE);
-        float h = start == bos ? (p.h0 ? p.h0[(size_t)s * p.dim + c] : 0.f) : p.states[(size_t)(start / LR_TILE) * p.dim + c];
-        for (int t = start; t < end; ++t) {
-            float a, rest;
-            decay(load_scalar(p.g, (size_t)t * p.g_ts + c, p.gate_dtype), a, rest);
-            const float x = load_scalar(p.x, (size_t)t * p.x_ts + c, p.dtype);
-            before[t - start] = h;
-            h = fmaf(a, h, p.complement ? rest * x : x);
-        }
-        for (int t = end - 1; t >= start; --t) {
-            float a, rest;
-            decay(load_scalar(p.g, (size_t)t * p.g_ts + c, p.gate_dtype), a, rest);
-            const float x = load_scalar(p.x, (size_t)t * p.x_ts + c, p.dtype);
-            const float lam = load_scalar(p.dh, (size_t)t * p.dh_ts + c, p.dtype) + mu;
-            const float prev = p.complement ? before[t - start] - x : before[t - start];
-            mu = a * lam;
-            store_scalar(p.dx, (size_t)t * p.dim + c, p.complement ? rest * lam : lam, p.dtype);
-            store_scalar(p.dg, (size_t)t * p.dim + c, mu * prev, p.gate_dtype);
-        }
-        end = start;
-    }
-    if (p.dh0) p.dh0[(size_t)s * p.dim + c] = mu;
-}
-
-__global__ void k10_step(const StepParams p) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t i = blockIdx.y;
-    if (c >= p.dim) return;
-    const int64_t slot = p.slots ? p.slots[i] : i;
-    float y = 0.f;
-    if (slot >= 0 && slot < p.num_slots) {
-        float a, rest;
-        decay(load_scalar(p.g, (size_t)i * p.g_ts + c, p.gate_dtype), a, rest);
-        const float x = load_scalar(p.x, (size_t)i * p.x_ts + c, p.dtype);
-        float *h = p.state + (size_t)slot * p.dim + c;
-        y = fmaf(a, *h, p.complement ? rest * x : x);
-        *h = y;
-    }
-    store_scalar(p.y, (size_t)i * p.dim + c, y, p.dtype);
-}
-
 }  // namespace
 
-cudaError_t launch_linrec_fwd(const LinrecParams &p, cudaStream_t stream) {
-    k10_fwd<<<dim3((p.dim + 127) / 128, p.N), 128, 0, stream>>>(p);
-    return cudaGetLastError();
+// status and ticket, the flags (for the narrowest blocks, 32 channels), then the records
+size_t linrec_workspace(int64_t rows, int64_t dim) {
+    const int64_t tiles = (rows + LR_TILE - 1) / LR_TILE;
+    if (tiles <= LR_WALK) return 256;
+    int64_t n[4];
+    tree_sizes(tiles, n);
+    size_t bytes = 256;
+    for (int level = 0; level < 4; ++level) bytes += up(sizeof(int) * (size_t)(n[level] * ((dim + 31) / 32)));
+    for (int level = 0; level < 4; ++level) bytes += up(sizeof(float2) * (size_t)(n[level] * dim));
+    return bytes;
 }
-cudaError_t launch_linrec_bwd(const LinrecParams &p, cudaStream_t stream) {
-    k10_bwd<<<dim3((p.dim + 127) / 128, p.N), 128, 0, stream>>>(p);
-    return cudaGetLastError();
+
+// Places the tree in the workspace for blocks of `channels` and clears what has to start at zero.
+cudaError_t linrec_blocks(LinrecParams &p, int channels, cudaStream_t stream) {
+    p.tiles = p.rows > 0 ? (p.rows + LR_TILE - 1) / LR_TILE : 1;
+    p.nblk = (p.dim + channels - 1) / channels;
+    p.walk = p.tiles <= LR_WALK;
+    p.blocks = FastDiv::of((uint32_t)p.nblk);
+    p.per_seq = FastDiv::of((uint32_t)(p.tokens > 0 ? p.tokens : 1));
+    if (p.walk) {
+        p.grid = (unsigned)p.nblk;
+        return cudaSuccess;
+    }
+    const int64_t grid = (int64_t)p.tiles * p.nblk;
+    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    p.grid = (unsigned)grid;
+    int64_t n[4];
+    tree_sizes(p.tiles, n);
+    char *at = reinterpret_cast<char *>(p.status) + 256;
+    for (int level = 0; level < 4; ++level) {
+        p.flags[level] = reinterpret_cast<int *>(at);
+        at += up(sizeof(int) * (size_t)(n[level] * p.nblk));
+    }
+    const size_t cleared = at - reinterpret_cast<char *>(p.status);
+    for (int level = 0; level < 4; ++level) {
+        p.recs[level] = reinterpret_cast<float2 *>(at);
+        at += up(sizeof(float2) * (size_t)(n[level] * p.dim));
+    }
+    p.ticket = p.status + 1;
+    return cudaMemsetAsync(p.status, 0, cleared, stream);
 }
-cudaError_t launch_linrec_step(const StepParams &p, cudaStream_t stream) {
-    k10_step<<<dim3((p.dim + 127) / 128, (unsigned)p.batch), 128, 0, stream>>>(p);
-    return cudaGetLastError();
+
+template <typename T, typename G> cudaError_t linrec_fwd_t(LinrecParams &, cudaStream_t);
+template <typename T, typename G> cudaError_t linrec_bwd_t(LinrecParams &, cudaStream_t);
+template <typename T, typename G> cudaError_t linrec_step_t(StepParams &, cudaStream_t);
+
+#define BY_TYPES(p, CALL)                                                       \
+    do {                                                                        \
+        if (p.dtype == F32) return CALL(float, float);                          \
+        if (p.dtype == BF16 && p.gate_dtype == F32) return CALL(__nv_bfloat16, float); \
+        if (p.dtype == BF16) return CALL(__nv_bfloat16, __nv_bfloat16);         \
+        if (p.gate_dtype == F32) return CALL(__half, float);                    \
+        return CALL(__half, __half);                                            \
+    } while (0)
+
+cudaError_t launch_linrec_fwd(LinrecParams p, cudaStream_t stream) {
+#define CALL(T, G) linrec_fwd_t<T, G>(p, stream)
+    BY_TYPES(p, CALL);
+#undef CALL
+}
+cudaError_t launch_linrec_bwd(LinrecParams p, cudaStream_t stream) {
+#define CALL(T, G) linrec_bwd_t<T, G>(p, stream)
+    BY_TYPES(p, CALL);
+#undef CALL
+}
+cudaError_t launch_linrec_step(StepParams p, cudaStream_t stream) {
+#define CALL(T, G) linrec_step_t<T, G>(p, stream)
+    BY_TYPES(p, CALL);
+#undef CALL
 }
 
 }  // namespace gdr
