@@ -362,7 +362,7 @@ def linrec_fwd(x, g, h0=None, cu_seqlens=None, *, complement=False, return_state
     x [B, T, D] (fp32, bf16 or fp16); g [B, T, D] the raw log-gate, of x's type or fp32; h0 fp32 [N, D] or None (zero);
     cu_seqlens int32 [N + 1] (packed sequences, B == 1) or None (N = B).  The last axis of x and g is contiguous and the
     others at one distance.  Returns (h like x, ht fp32 [N, D]), and with ``return_states`` the states fp32
-    [ceil(B T / 64), D] that :func:`linrec_bwd` takes.  ``check_status`` waits for the call and raises on malformed
+    [ceil(B T / 128), D] that :func:`linrec_bwd` takes.  ``check_status`` waits for the call and raises on malformed
     cu_seqlens."""
     if stream is not None:
         with _on(stream, (x, g, h0, cu_seqlens)):
@@ -427,7 +427,7 @@ def linrec_bwd(x, g, dh, h0=None, dht=None, cu_seqlens=None, states=None, *, com
 
 class LinearRecurrence(torch.autograd.Function):
     """h, ht = forward(x, g, h0, cu_seqlens, complement) with its exact backward.  The inputs and one fp32 state for
-    every 64 tokens are saved."""
+    every 128 tokens are saved."""
 
     @staticmethod
     def forward(ctx, x, g, h0, cu_seqlens, complement):

@@ -214,7 +214,7 @@ gdr_status gdr_add_norm_bwd(const gdr_add_norm_bwd_args *a, void *stream_) {
 // ---------------------------------------------------------------- gated linear recurrence
 size_t gdr_linrec_workspace_bytes(int64_t rows, int64_t dim) {
     if (rows < 0 || rows > kMaxRows || dim < 1) return 0;
-    return linrec_workspace(rows, dim);
+    return 256;  // the status word
 }
 
 static gdr_status linrec_sizes(int64_t batch, int64_t tokens, int64_t dim, int64_t num_seqs, int dtype, int gate_dtype,
@@ -224,9 +224,12 @@ static gdr_status linrec_sizes(int64_t batch, int64_t tokens, int64_t dim, int64
         return GDR_ERR_INVALID_ARG;
     if (batch > kMaxRows || tokens > kMaxRows || batch * tokens > kMaxRows || dim > (1 << 20) || num_seqs > (1 << 24))
         return GDR_ERR_UNSUPPORTED;
-    // (tiles x blocks of 32 channels number the CTAs)
-    if ((batch * tokens / GDR_LINREC_TILE + 1) * ((dim + 31) / 32) >= (1ll << 31)) return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
+}
+
+// Rows that a tensor map can describe: apart from each other, at a distance that its 40 bits hold.
+static bool map_rows(int64_t stride, int64_t rows, int64_t dim) {
+    return rows <= 1 || (stride >= dim && stride < (1ll << 36));
 }
 
 static uint32_t spin_limit() {
@@ -246,7 +249,7 @@ gdr_status gdr_linrec_fwd(const gdr_linrec_fwd_args *a, void *stream_) {
     if (!a->workspace || !at(a->workspace, 256) || a->workspace_bytes < gdr_linrec_workspace_bytes(rows, a->dim))
         return GDR_ERR_INVALID_ARG;
     if (!at(a->h0, 4) || !at(a->ht, 4) || !at(a->states, 4) || !at(a->cu_seqlens, 4)) return GDR_ERR_INVALID_ARG;
-    VecRule v(4);
+    VecRule v(8);  // tensor maps take multiples of 16 bytes
     v.tensor(a->x, a->dtype, a->x_token_stride);
     v.tensor(a->g, a->gate_dtype, a->g_token_stride);
     v.tensor(a->h, a->dtype, a->dim);
@@ -261,7 +264,7 @@ gdr_status gdr_linrec_fwd(const gdr_linrec_fwd_args *a, void *stream_) {
     p.rows = (int)rows, p.tokens = (int)a->tokens, p.dim = (int)a->dim;
     p.N = (int)(a->num_seqs > 0 ? a->num_seqs : a->batch), p.complement = a->complement;
     p.dtype = a->dtype, p.gate_dtype = a->gate_dtype;
-    p.vec = v.ok;
+    p.vec = v.ok && rows > 0 && map_rows(a->x_token_stride, rows, a->dim) && map_rows(a->g_token_stride, rows, a->dim);
     p.status = (int *)a->workspace, p.spin = spin_limit();
     return done(launch_linrec_fwd(p, stream));
 }
@@ -280,7 +283,7 @@ gdr_status gdr_linrec_bwd(const gdr_linrec_bwd_args *a, void *stream_) {
         return GDR_ERR_INVALID_ARG;
     if (!at(a->h0, 4) || !at(a->dht, 4) || !at(a->states, 4) || !at(a->dh0, 4) || !at(a->cu_seqlens, 4))
         return GDR_ERR_INVALID_ARG;
-    VecRule v(4);
+    VecRule v(8);  // tensor maps take multiples of 16 bytes
     v.tensor(a->x, a->dtype, a->x_token_stride);
     v.tensor(a->g, a->gate_dtype, a->g_token_stride);
     v.tensor(a->dh, a->dtype, a->dh_token_stride);
@@ -299,7 +302,8 @@ gdr_status gdr_linrec_bwd(const gdr_linrec_bwd_args *a, void *stream_) {
     p.rows = (int)rows, p.tokens = (int)a->tokens, p.dim = (int)a->dim;
     p.N = (int)(a->num_seqs > 0 ? a->num_seqs : a->batch), p.complement = a->complement;
     p.dtype = a->dtype, p.gate_dtype = a->gate_dtype;
-    p.vec = v.ok;
+    p.vec = v.ok && rows > 0 && map_rows(a->x_token_stride, rows, a->dim) && map_rows(a->g_token_stride, rows, a->dim) &&
+            map_rows(a->dh_token_stride, rows, a->dim);
     p.status = (int *)a->workspace, p.spin = spin_limit();
     return done(launch_linrec_bwd(p, stream));
 }

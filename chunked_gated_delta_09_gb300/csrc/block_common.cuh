@@ -73,8 +73,8 @@ struct AddNormParams {
     bool vec;
 };
 
-// Rows of a tile of the recurrence's scans; a state is saved for each.
-constexpr int LR_TILE = 64;
+// Rows of the recurrence between saved states, and of a tile of its backward; channels of a tile; CTAs of a cluster.
+constexpr int LR_TILE = 128, LR_CH = 32, LR_MAX_CLUSTER = 16;
 
 struct LinrecParams {
     const void *x, *g, *dh;
@@ -85,16 +85,25 @@ struct LinrecParams {
     int64_t x_ts, g_ts, dh_ts;
     int rows, tokens, dim, N, complement;  // rows = batch * tokens; N sequences
     int dtype, gate_dtype;
-    bool vec;   // rows are moved in pieces of several elements
-    bool walk;  // one CTA walks all tiles of its channels
+    bool vec;    // rows can be moved by tensor maps
+    bool clear;  // the kernel clears the status word
     uint32_t spin;
-    // the workspace: a status word, the ticket, and the tree of maps (tiles, groups, blocks, spans)
-    int *status, *ticket;
-    int *flags[4];    // [record][block of channels]
-    float2 *recs[4];  // [record][dim]
-    int tiles, nblk;  // tiles of rows, blocks of channels
-    unsigned grid;
-    FastDiv blocks, per_seq;  // divide by nblk, by tokens
+    int *status;
+    int tiles, cluster, supers;  // tiles of rows, CTAs of a cluster, clusters' worth of rows
+    FastDiv per_seq;             // divides by tokens
+};
+
+struct LinrecMaps {
+    CUtensorMap g, x, dh;
+};
+
+// A launch of a kernel of the recurrence: what is known of it beforehand, and the configuration that linrec_plan makes.
+struct LinrecLaunch {
+    const void *kernel;
+    int threads, smem;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = {};
+    LinrecLaunch(const void *k, int t, int s) : kernel(k), threads(t), smem(s) {}
 };
 
 struct StepParams {
@@ -116,8 +125,12 @@ cudaError_t launch_gated_norm_fwd(const GatedNormParams &p, cudaStream_t stream)
 cudaError_t launch_gated_norm_bwd(const GatedNormParams &p, cudaStream_t stream);
 cudaError_t launch_add_norm_fwd(const AddNormParams &p, cudaStream_t stream);
 cudaError_t launch_add_norm_bwd(const AddNormParams &p, cudaStream_t stream);
-size_t linrec_workspace(int64_t rows, int64_t dim);
-cudaError_t linrec_blocks(LinrecParams &p, int channels, cudaStream_t stream);
+cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, cudaStream_t stream);
+cudaError_t linrec_maps(const LinrecParams &p, LinrecMaps &maps, int rows_per_tile);
+// Tensor map of rows [rows][dim] at a distance of `stride` elements, for boxes of box_rows x box_cols; what lies outside
+// reads as zero.  Base, stride and box_cols in bytes must be multiples of 16.
+cudaError_t encode_matrix_map(CUtensorMap *map, const void *base, int dtype, int64_t rows, int64_t dim, int64_t stride,
+                              int box_rows, int box_cols);
 cudaError_t launch_linrec_fwd(LinrecParams p, cudaStream_t stream);
 cudaError_t launch_linrec_bwd(LinrecParams p, cudaStream_t stream);
 cudaError_t launch_linrec_step(StepParams p, cudaStream_t stream);

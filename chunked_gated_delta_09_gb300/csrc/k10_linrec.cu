@@ -1,74 +1,103 @@
-// k10_linrec.cu -- the gated linear recurrence: workspace, grid, and choice by type.
+// k10_linrec.cu -- the gated linear recurrence: cluster and grid, tensor maps, and choice by type.
+#include <mutex>
+#include <unordered_map>
+
 #include "block_common.cuh"
 
 namespace gdr {
-
-// A sequence of up to this many tiles is walked by one CTA per block of channels: a tile takes it about 2 us, and the
-// tree's cleared flags and hops cost more than that until there are as many.
-constexpr int LR_WALK = 4;
-
 namespace {
-size_t up(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Records at each level of the tree over `tiles` tiles.
-void tree_sizes(int64_t tiles, int64_t (&n)[4]) {
-    for (int level = 0; level < 4; ++level) n[level] = (tiles + ((int64_t)1 << (3 * level)) - 1) >> (3 * level);
+// For clusters of 1, 2, 4, 8 and 16 CTAs: how many clusters of a kernel the device holds at a time (0: none).
+struct Resident {
+    int clusters[5];
+};
+std::mutex g_mu;
+std::unordered_map<const void *, Resident> g_resident[64];  // per device
+
+cudaError_t resident(LinrecLaunch &l, Resident &out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (dev >= 0 && dev < 64) {
+        auto it = g_resident[dev].find(l.kernel);
+        if (it != g_resident[dev].end()) {
+            out = it->second;
+            return cudaSuccess;
+        }
+    }
+    if ((e = cudaFuncSetAttribute(l.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, l.smem)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(l.kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+    for (int k = 0; k < 5; ++k) {
+        l.cfg.gridDim = dim3(16);
+        l.attr.val.clusterDim.x = 1u << k;
+        if (cudaOccupancyMaxActiveClusters(&out.clusters[k], l.kernel, &l.cfg) != cudaSuccess) {
+            cudaGetLastError();
+            out.clusters[k] = 0;
+        }
+    }
+    if (out.clusters[0] < 1) return cudaErrorInvalidConfiguration;
+    if (dev >= 0 && dev < 64) g_resident[dev][l.kernel] = out;
+    return cudaSuccess;
 }
+
 }  // namespace
 
-// status and ticket, the flags (for the narrowest blocks, 32 channels), then the records
-size_t linrec_workspace(int64_t rows, int64_t dim) {
-    const int64_t tiles = (rows + LR_TILE - 1) / LR_TILE;
-    if (tiles <= LR_WALK) return 256;
-    int64_t n[4];
-    tree_sizes(tiles, n);
-    size_t bytes = 256;
-    for (int level = 0; level < 4; ++level) bytes += up(sizeof(int) * (size_t)(n[level] * ((dim + 31) / 32)));
-    for (int level = 0; level < 4; ++level) bytes += up(sizeof(float2) * (size_t)(n[level] * dim));
-    return bytes;
+// Chooses the cluster's size and the grid for tiles of `rows_per_tile` rows x 32 channels.
+cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, cudaStream_t stream) {
+    l.cfg = {};
+    l.cfg.blockDim = dim3((unsigned)l.threads);
+    l.cfg.dynamicSmemBytes = (size_t)l.smem;
+    l.cfg.stream = stream;
+    l.attr.id = cudaLaunchAttributeClusterDimension;
+    l.attr.val.clusterDim.x = l.attr.val.clusterDim.y = l.attr.val.clusterDim.z = 1;
+    l.cfg.attrs = &l.attr;
+    l.cfg.numAttrs = 1;
+    Resident r;
+    cudaError_t e = resident(l, r);
+    if (e != cudaSuccess) return e;
+    p.tiles = p.rows > 0 ? (p.rows + rows_per_tile - 1) / rows_per_tile : 1;
+    p.per_seq = FastDiv::of((uint32_t)(p.tokens > 0 ? p.tokens : 1));
+    const int64_t nblk = (p.dim + LR_CH - 1) / LR_CH;
+    // the size whose clusters take the fewest tiles one after the other, all waves of them together; of equal ones the
+    // smallest
+    int64_t best = -1;
+    for (int k = 0; k < 5; ++k) {
+        const int size = 1 << k;
+        if (r.clusters[k] < 1 || (k > 0 && size / 2 >= p.tiles)) continue;
+        const int64_t waves = (nblk + r.clusters[k] - 1) / r.clusters[k], turns = waves * ((p.tiles + size - 1) / size);
+        if (best < 0 || turns < best) best = turns, p.cluster = size;
+    }
+    if (const char *w = getenv("LR_CLUSTER")) p.cluster = atoi(w);
+    p.supers = (p.tiles + p.cluster - 1) / p.cluster;
+    l.cfg.gridDim = dim3((unsigned)(nblk * p.cluster));
+    l.attr.val.clusterDim.x = (unsigned)p.cluster;
+    // malformed cu_seqlens, or waits that a short limit makes expire, may be noted before any CTA could clear the word
+    p.clear = !p.cu && p.spin >= (1u << 16);
+    return p.clear ? cudaSuccess : cudaMemsetAsync(p.status, 0, sizeof(int), stream);
 }
 
-// Places the tree in the workspace for blocks of `channels` and clears what has to start at zero.
-cudaError_t linrec_blocks(LinrecParams &p, int channels, cudaStream_t stream) {
-    p.tiles = p.rows > 0 ? (p.rows + LR_TILE - 1) / LR_TILE : 1;
-    p.nblk = (p.dim + channels - 1) / channels;
-    p.walk = p.tiles <= LR_WALK;
-    p.blocks = FastDiv::of((uint32_t)p.nblk);
-    p.per_seq = FastDiv::of((uint32_t)(p.tokens > 0 ? p.tokens : 1));
-    if (p.walk) {
-        p.grid = (unsigned)p.nblk;
-        return cudaSuccess;
-    }
-    const int64_t grid = (int64_t)p.tiles * p.nblk;
-    if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    p.grid = (unsigned)grid;
-    int64_t n[4];
-    tree_sizes(p.tiles, n);
-    char *at = reinterpret_cast<char *>(p.status) + 256;
-    for (int level = 0; level < 4; ++level) {
-        p.flags[level] = reinterpret_cast<int *>(at);
-        at += up(sizeof(int) * (size_t)(n[level] * p.nblk));
-    }
-    const size_t cleared = at - reinterpret_cast<char *>(p.status);
-    for (int level = 0; level < 4; ++level) {
-        p.recs[level] = reinterpret_cast<float2 *>(at);
-        at += up(sizeof(float2) * (size_t)(n[level] * p.dim));
-    }
-    p.ticket = p.status + 1;
-    return cudaMemsetAsync(p.status, 0, cleared, stream);
+cudaError_t linrec_maps(const LinrecParams &p, LinrecMaps &maps, int rows_per_tile) {
+    auto one = [&](CUtensorMap &map, const void *base, int dtype, int64_t stride) {
+        return encode_matrix_map(&map, base, dtype, p.rows, p.dim, p.rows > 1 ? stride : p.dim, rows_per_tile, LR_CH);
+    };
+    cudaError_t e = one(maps.g, p.g, p.gate_dtype, p.g_ts);
+    if (e == cudaSuccess) e = one(maps.x, p.x, p.dtype, p.x_ts);
+    if (e == cudaSuccess && p.dh) e = one(maps.dh, p.dh, p.dtype, p.dh_ts);
+    return e;
 }
 
 template <typename T, typename G> cudaError_t linrec_fwd_t(LinrecParams &, cudaStream_t);
 template <typename T, typename G> cudaError_t linrec_bwd_t(LinrecParams &, cudaStream_t);
 template <typename T, typename G> cudaError_t linrec_step_t(StepParams &, cudaStream_t);
 
-#define BY_TYPES(p, CALL)                                                       \
-    do {                                                                        \
-        if (p.dtype == F32) return CALL(float, float);                          \
+#define BY_TYPES(p, CALL)                                                              \
+    do {                                                                               \
+        if (p.dtype == F32) return CALL(float, float);                                 \
         if (p.dtype == BF16 && p.gate_dtype == F32) return CALL(__nv_bfloat16, float); \
-        if (p.dtype == BF16) return CALL(__nv_bfloat16, __nv_bfloat16);         \
-        if (p.gate_dtype == F32) return CALL(__half, float);                    \
-        return CALL(__half, __half);                                            \
+        if (p.dtype == BF16) return CALL(__nv_bfloat16, __nv_bfloat16);                \
+        if (p.gate_dtype == F32) return CALL(__half, float);                           \
+        return CALL(__half, __half);                                                   \
     } while (0)
 
 cudaError_t launch_linrec_fwd(LinrecParams p, cudaStream_t stream) {

@@ -102,7 +102,7 @@ size_t gdr_norm_workspace_bytes(int64_t rows, int64_t dim, int sums);
  * workspace: gdr_linrec_workspace_bytes(batch * tokens, dim) bytes, 256-byte aligned, not used by another call
  * that may run at the same time.  Malformed cu_seqlens and waits that expire are read with
  * gdr_linrec_get_status. */
-#define GDR_LINREC_TILE 64
+#define GDR_LINREC_TILE 128
 typedef struct {
     const void *x, *g;
     const float *h0;
