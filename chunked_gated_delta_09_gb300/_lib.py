@@ -24,7 +24,7 @@ BLOCK_EXPORTS = ("gdr_gated_norm_fwd", "gdr_gated_norm_bwd", "gdr_add_norm_fwd",
                  "gdr_clip_workspace_bytes")
 NOALLOC_MAX_WORKSPACE = 64 << 20
 NORM_MAX_DIM = 16384
-LINREC_TILE = 128
+LINREC_SAVE = 16
 NUM_STAGES = 6
 STAGE_NAMES = ("k0_chunk_indices", "k1_wy_prep", "k2_fused_gdr_h", "k3_dh_scan", "k4_intra_grad", "k5_dg_reduce")
 

@@ -362,7 +362,7 @@ def linrec_fwd(x, g, h0=None, cu_seqlens=None, *, complement=False, return_state
     x [B, T, D] (fp32, bf16 or fp16); g [B, T, D] the raw log-gate, of x's type or fp32; h0 fp32 [N, D] or None (zero);
     cu_seqlens int32 [N + 1] (packed sequences, B == 1) or None (N = B).  The last axis of x and g is contiguous and the
     others at one distance.  Returns (h like x, ht fp32 [N, D]), and with ``return_states`` the states fp32
-    [ceil(B T / 128), D] that :func:`linrec_bwd` takes.  ``check_status`` waits for the call and raises on malformed
+    [ceil(B T / 16), D] that :func:`linrec_bwd` takes.  ``check_status`` waits for the call and raises on malformed
     cu_seqlens."""
     if stream is not None:
         with _on(stream, (x, g, h0, cu_seqlens)):
@@ -372,7 +372,7 @@ def linrec_fwd(x, g, h0=None, cu_seqlens=None, *, complement=False, return_state
     dev = x.device
     h = torch.empty(x.shape, dtype=x.dtype, device=dev)
     ht = torch.empty(N, D, dtype=_F32, device=dev)
-    tiles = -(-B * T // _lib.LINREC_TILE)
+    tiles = -(-B * T // _lib.LINREC_SAVE)
     states = torch.empty(tiles, D, dtype=_F32, device=dev) if return_states else None
     nbytes = _lib.load().gdr_linrec_workspace_bytes(B * T, D)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -401,7 +401,7 @@ def linrec_bwd(x, g, dh, h0=None, dht=None, cu_seqlens=None, states=None, *, com
     dev = x.device
     nbytes = _lib.load().gdr_linrec_workspace_bytes(B * T, D)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    tiles = -(-B * T // _lib.LINREC_TILE)
+    tiles = -(-B * T // _lib.LINREC_SAVE)
     strides = _token_stride(x, "x"), _token_stride(g, "g")
     seqs = 0 if cu_seqlens is None else N
     if states is None:
@@ -427,7 +427,7 @@ def linrec_bwd(x, g, dh, h0=None, dht=None, cu_seqlens=None, states=None, *, com
 
 class LinearRecurrence(torch.autograd.Function):
     """h, ht = forward(x, g, h0, cu_seqlens, complement) with its exact backward.  The inputs and one fp32 state for
-    every 128 tokens are saved."""
+    every 16 tokens are saved."""
 
     @staticmethod
     def forward(ctx, x, g, h0, cu_seqlens, complement):

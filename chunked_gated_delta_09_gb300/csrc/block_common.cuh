@@ -73,8 +73,8 @@ struct AddNormParams {
     bool vec;
 };
 
-// Rows of the recurrence between saved states, and of a tile of its backward; channels of a tile; CTAs of a cluster.
-constexpr int LR_TILE = 128, LR_CH = 32, LR_MAX_CLUSTER = 16;
+// Rows of the recurrence between saved states; channels of a tile; CTAs of a cluster, at most.
+constexpr int LR_SAVE = 16, LR_CH = 32, LR_MAX_CLUSTER = 16;
 
 struct LinrecParams {
     const void *x, *g, *dh;

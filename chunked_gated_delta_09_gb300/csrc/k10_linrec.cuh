@@ -7,13 +7,13 @@
 // whatever the sequences: where a sequence starts (or, backwards, ends) inside a tile, the row's map forgets what
 // came before it (a flag rather than A = 0, so that a nan does not pass from one sequence to the next).
 //
-// A cluster of CTAs owns a block of 32 channels and goes through all rows, a tile for each CTA at a time.  A warp
-// composes 16 rows of its CTA's tile (two groups of 8, 16 lanes with two channels each) and keeps a and b in registers;
-// the warps' maps are composed in shared memory, and the CTA's map is sent to every CTA of the cluster, which then
-// knows the state that enters its own tile and finishes its rows.  So every value is read once and written once, nothing
-// is exchanged through memory, and the order of all sums is fixed: results are bit-identical from run to run.  The next
-// tiles arrive by tensor-map loads meanwhile.  The forward saves the state that enters each LR_TILE rows, from which the
-// backward recomputes h instead of reading it back rounded.
+// A cluster of CTAs owns a block of 32 channels and goes through all rows, a tile for each CTA at a time.  Eight lanes
+// with four channels each compose a group of 8 (backwards 4) rows and keep a and b in registers; the groups' maps are
+// composed by warp scans over shared memory, and the tile's map is sent to every CTA of the cluster, which then knows
+// the state that enters its own tile and finishes its rows.  So every value is read once and written once, nothing is
+// exchanged through memory, and the order of all sums is fixed: results are bit-identical from run to run.  The next
+// tiles arrive by tensor-map loads meanwhile.  The forward saves the state that enters each LR_SAVE rows (a warp's rows of
+// the backward), from which the backward recomputes h instead of reading it back rounded.
 #pragma once
 
 #include "block_common.cuh"
@@ -26,10 +26,10 @@ using tc::mbar_expect_tx;
 using tc::mbar_init;
 using tc::mbar_wait;
 
-constexpr int LR_WROWS = 16;      // rows of a warp: two groups of 8
-constexpr int LR_FWD_WARPS = 16;  // 256 rows
-constexpr int LR_BWD_WARPS = LR_TILE / LR_WROWS;
-constexpr int LR_FWD_STAGES = 2, LR_BWD_STAGES = 3;
+constexpr int LR_WARPS = 8, LR_THREADS = 32 * LR_WARPS;
+constexpr int LR_GROUPS = 32;                // of a tile, 4 to a warp
+constexpr int LR_FWD_R = 8, LR_BWD_R = 4;    // rows of a group
+static_assert(LR_SAVE == 4 * LR_BWD_R, "a saved state enters each warp's rows of the backward");
 
 // ---------------------------------------------------------------- pairs of fp32 values, one instruction for both
 struct F2 {
@@ -54,12 +54,6 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
     return d;
 }
-__device__ __forceinline__ F2 shfl2(F2 a, int lane) {
-    float x, y;
-    a.get(x, y);
-    return F2(__shfl_sync(0xffffffffu, x, lane), __shfl_sync(0xffffffffu, y, lane));
-}
-
 // exp(g) and 1 - exp(g), both to about one unit in the last place and without a lean to one side, which a channel that
 // remembers hundreds of tokens would add up (decays near 1 that come out a quarter of a unit too low put h off by
 // 1e-5).  Cody and Waite's reduction g = n ln 2 + r, then exp(r) - 1 = r + r^2 q(r) with q a Chebyshev fit of degree 4
@@ -85,18 +79,71 @@ __device__ __forceinline__ void decay2(float g0, float g1, F2 &a, F2 &rest) {
     rest = fma2(p, ns, add2(one, ns));
 }
 
-// ---------------------------------------------------------------- maps
-// The map s -> a s + b, or b where what came before is cut off.
-struct Map {
-    float a = 1.f, b = 0.f;
-    bool cut = false;
-    __device__ __forceinline__ void then(float a2, float b2, bool cut2) {
-        b = cut2 ? b2 : fmaf(a2, b, b2);
-        a *= a2;
-        cut |= cut2;
-    }
-    __device__ __forceinline__ float of(float s) const { return cut ? b : fmaf(a, s, b); }
+// Four neighbouring channels of a row.
+struct F4 {
+    F2 lo, hi;
 };
+__device__ __forceinline__ F4 fma4(F4 a, F4 b, F4 c) { return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)}; }
+__device__ __forceinline__ F4 mul4(F4 a, F4 b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
+__device__ __forceinline__ F4 add4(F4 a, F4 b) { return {add2(a.lo, b.lo), add2(a.hi, b.hi)}; }
+__device__ __forceinline__ F4 make4(float x, float y, float z, float w) { return {F2(x, y), F2(z, w)}; }
+__device__ __forceinline__ F4 make4(const float4 &v) { return make4(v.x, v.y, v.z, v.w); }
+
+// ---------------------------------------------------------------- maps
+// The maps of W groups (or warps).  Rows of 33 put the lanes of a scan on different banks.
+template <int W> using Maps = float2[W][LR_CH + 1];
+
+template <int W> __device__ __forceinline__ void put_maps(Maps<W> &at, int w, int ch, F4 a, F4 b) {
+    float x, y, u, v;
+    a.lo.get(x, y), b.lo.get(u, v);
+    at[w][ch] = make_float2(x, u), at[w][ch + 1] = make_float2(y, v);
+    a.hi.get(x, y), b.hi.get(u, v);
+    at[w][ch + 2] = make_float2(x, u), at[w][ch + 3] = make_float2(y, v);
+}
+
+// Composes W maps along the scan (from the last to the first with BACK): in place each becomes the map of the rows before
+// it, and `total` that of all of them.  A warp takes 4 channels, W / 8 to a lane, a lane for each position of the scan,
+// and composes over distances 1, 2, 4 ...; bit j of cuts: the map at position j cuts off what came before.
+template <int W, bool BACK>
+__device__ __forceinline__ void scan_maps(Maps<W> &maps, uint32_t cuts, int wid, int lane, float2 *total) {
+    constexpr int N = W / 8;  // channels of a lane
+    const int j = lane % W, ch = 4 * wid + lane / W;
+    float2 *at = &maps[BACK ? W - 1 - j : j][ch];
+    float a[N], b[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = at[i].x, b[i] = at[i].y;
+#pragma unroll
+    for (int d = 1; d < W; d *= 2) {
+        const bool cut = cuts && (cuts >> ((j - d + 1) & 31)) & ((1u << d) - 1);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float a1 = __shfl_up_sync(0xffffffffu, a[i], d, W), b1 = __shfl_up_sync(0xffffffffu, b[i], d, W);
+            if (j >= d) {
+                if (!cut) b[i] = fmaf(a[i], b1, b[i]);
+                a[i] *= a1;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (j == W - 1) total[ch + i] = make_float2(a[i], b[i]);
+        const float a1 = __shfl_up_sync(0xffffffffu, a[i], 1, W), b1 = __shfl_up_sync(0xffffffffu, b[i], 1, W);
+        at[i] = j ? make_float2(a1, b1) : make_float2(1.f, 0.f);
+    }
+}
+// Four channels' states taken through the map that scan_maps left; cut: that map cuts off.
+template <int W> __device__ __forceinline__ F4 through(const Maps<W> &maps, int w, int ch, bool cut, const float *s) {
+    const float2 *m = &maps[w][ch];
+    const float2 m0 = m[0], m1 = m[1], m2 = m[2], m3 = m[3];
+    const F4 b = make4(m0.y, m1.y, m2.y, m3.y);
+    return cut ? b : fma4(make4(m0.x, m1.x, m2.x, m3.x), make4(*reinterpret_cast<const float4 *>(s + ch)), b);
+}
+__device__ __forceinline__ F4 shfl4(F4 v, int lane) {
+    float x, y, z, w;
+    v.lo.get(x, y), v.hi.get(z, w);
+    return make4(__shfl_sync(0xffffffffu, x, lane), __shfl_sync(0xffffffffu, y, lane), __shfl_sync(0xffffffffu, z, lane),
+                 __shfl_sync(0xffffffffu, w, lane));
+}
 
 __device__ __forceinline__ int cluster_rank() {
     int r;
@@ -144,12 +191,12 @@ struct Peers {
     float2 map[2][LR_MAX_CLUSTER][LR_CH];
     int cut[2][LR_MAX_CLUSTER];
     uint64_t bar[2];
-    // one warp, a lane for each channel
-    __device__ __forceinline__ void tell(int buf, int rank, int size, const Map &m) {
+    // by one warp: this CTA's map, a lane for each channel, to all
+    __device__ __forceinline__ void tell(int buf, int rank, int size, float2 m, bool c) {
         const int lane = threadIdx.x & 31;
         if (lane == 0) mbar_expect_tx(&bar[buf], (uint32_t)size * (LR_CH * 8 + 4));
         uint64_t v;
-        asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(m.a), "f"(m.b));
+        asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(m.x), "f"(m.y));
         for (int q = 0; q < size; ++q) {
             const uint32_t b = in_cta(&bar[buf], q);
             asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
@@ -159,90 +206,95 @@ struct Peers {
             if (lane == 0)
                 asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
                                  in_cta(&cut[buf][rank], q)),
-                             "r"((int)m.cut), "r"(b)
+                             "r"((int)c), "r"(b)
                              : "memory");
         }
     }
-    // the state s taken through all tiles of the cluster, for a lane's channel
-    __device__ __forceinline__ float through(int buf, int size, float s) const {
+    // For a lane's channel, the state s that enters the cluster's rows taken through the tiles before that of CTA `rank`;
+    // s itself is taken through all of them.
+    __device__ __forceinline__ float entry(int buf, int rank, int size, float &s) const {
+        float at = s;
         for (int q = 0; q < size; ++q) {
             const float2 v = map[buf][q][threadIdx.x & 31];
+            if (q == rank) at = s;
             s = cut[buf][q] ? v.y : fmaf(v.x, s, v.y);
         }
-        return s;
-    }
-    // the states s taken through the tiles before that of CTA `rank`, for two channels
-    __device__ __forceinline__ F2 entry(int buf, int rank, int ch, F2 s) const {
-        for (int q = 0; q < rank; ++q) {
-            const float4 v = *reinterpret_cast<const float4 *>(&map[buf][q][ch]);
-            s = cut[buf][q] ? F2(v.y, v.w) : fma2(F2(v.x, v.z), s, F2(v.y, v.w));
-        }
-        return s;
+        return at;
     }
 };
 
 // ---------------------------------------------------------------- a tile's rows
-// First and last rows of sequences among a tile's ROWS rows, and the rows' sequences.
-template <int ROWS> struct Sequences {
-    uint32_t head[ROWS / 32], tail[ROWS / 32];
-    int seq[ROWS];
-    // the last sequence that starts at or before the row
-    static __device__ __forceinline__ int of_row(const LinrecParams &p, int row) {
-        if (!p.cu) return p.per_seq.div(row);
-        int lo = 0, hi = p.N;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (p.cu[mid] <= row) lo = mid;
-            else hi = mid;
-        }
-        return lo;
-    }
-    // by one warp
-    __device__ __forceinline__ void find(const LinrecParams &p, int tile) {
+// Which rows of a tile are the first or the last of a sequence.
+template <int R> struct Ends {
+    static constexpr int ROWS = R * LR_GROUPS;
+    uint32_t head[R], tail[R];  // a bit for each row
+    // by one warp; [a, b): the sequence that the warp met last, with which it goes on
+    __device__ __forceinline__ void find(const LinrecParams &p, int tile, int &a, int &b) {
         const int lane = threadIdx.x & 31, row0 = tile * ROWS, end = min(row0 + ROWS, p.rows);
-        bool none = row0 >= p.rows;
-        if (!none) {
-            const int s = of_row(p, row0), a = p.cu ? p.cu[s] : s * p.tokens, b = p.cu ? p.cu[s + 1] : a + p.tokens;
-            none = a < row0 && b > end;  // the tile lies within one sequence
+        if (row0 < p.rows && !(a <= row0 && row0 < b)) sequence_of(p, row0, a, b);
+        if (row0 >= p.rows || (a < row0 && b > end)) {  // the tile lies within one sequence, or has no rows
+            if (lane < R) head[lane] = tail[lane] = 0;
+            return;
         }
-        for (int k = 0; k < ROWS / 32; ++k) {
-            bool h = false, e = false;
-            if (!none) {
-                const int row = row0 + 32 * k + lane;
-                if (row < p.rows) {
-                    const int s = of_row(p, row), a = p.cu ? p.cu[s] : s * p.tokens, b = p.cu ? p.cu[s + 1] : a + p.tokens;
-                    h = a == row;
-                    e = b == row + 1;
-                    seq[32 * k + lane] = s;
-                }
-            }
-            const uint32_t hb = __ballot_sync(0xffffffffu, h), eb = __ballot_sync(0xffffffffu, e);
-            if (lane == 0) head[k] = hb, tail[k] = eb;
+        for (int k = 0; k < R; ++k) {
+            const int row = row0 + 32 * k + lane;
+            int from = -1, to = -1;
+            if (row < p.rows) sequence_of(p, row, from, to);
+            const uint32_t h = __ballot_sync(0xffffffffu, from == row), e = __ballot_sync(0xffffffffu, to == row + 1);
+            if (lane == 0) head[k] = h, tail[k] = e;
         }
     }
-    // of a warp's 16 rows
-    __device__ __forceinline__ uint32_t heads(int w) const { return head[w >> 1] >> (16 * (w & 1)) & 0xffff; }
-    __device__ __forceinline__ uint32_t tails(int w) const { return tail[w >> 1] >> (16 * (w & 1)) & 0xffff; }
+    // the last sequence that starts at or before the row, and its rows
+    static __device__ __forceinline__ int sequence_of(const LinrecParams &p, int row, int &a, int &b) {
+        int s;
+        if (p.cu) {
+            int hi = p.N;
+            s = 0;
+            while (hi - s > 1) {
+                const int mid = (s + hi) >> 1;
+                if (p.cu[mid] <= row) s = mid;
+                else hi = mid;
+            }
+            a = p.cu[s], b = p.cu[s + 1];
+        } else {
+            s = p.per_seq.div(row);
+            a = s * p.tokens, b = a + p.tokens;
+        }
+        return s;
+    }
+    static __device__ __forceinline__ int sequence_of(const LinrecParams &p, int row) {
+        int a, b;
+        return sequence_of(p, row, a, b);
+    }
+    // of a group's rows
+    __device__ __forceinline__ uint32_t heads(int g) const { return head[g * R / 32] >> (g * R % 32) & ((1u << R) - 1); }
+    __device__ __forceinline__ uint32_t tails(int g) const { return tail[g * R / 32] >> (g * R % 32) & ((1u << R) - 1); }
+    // bit per group: a sequence starts among its rows
+    __device__ __forceinline__ uint32_t head_cuts() const { return __ballot_sync(0xffffffffu, heads(threadIdx.x & 31)); }
+    // bit per warp, from the last one on: a sequence ends among its rows
+    __device__ __forceinline__ uint32_t tail_cuts() const {
+        const int w = LR_WARPS - 1 - (threadIdx.x & (LR_WARPS - 1)), n = 4 * R;
+        const uint32_t e = tail[w * n / 32] >> (w * n % 32) & (n < 32 ? (1u << (n & 31)) - 1 : 0xffffffffu);
+        return __ballot_sync(0xffffffffu, e) & ((1u << LR_WARPS) - 1);
+    }
 };
 
 // A tile of one tensor in shared memory: ROWS rows of 32 channels.
 template <typename T, int ROWS> struct Tile {
     T v[ROWS][LR_CH];
-    __device__ __forceinline__ void get(int r, int ch, float &x, float &y) const {
-        const Pack<T, 2> q = *reinterpret_cast<const Pack<T, 2> *>(&v[r][ch]);
-        x = to_f32(q.v[0]);
-        y = to_f32(q.v[1]);
+    __device__ __forceinline__ void get(int r, int ch, float (&o)[4]) const {
+        unpack<T, 4>(*reinterpret_cast<const Pack<T, 4> *>(&v[r][ch]), o);
     }
-    __device__ __forceinline__ F2 get(int r, int ch) const {
-        float x, y;
-        get(r, ch, x, y);
-        return F2(x, y);
+    __device__ __forceinline__ F4 get(int r, int ch) const {
+        float o[4];
+        get(r, ch, o);
+        return make4(o[0], o[1], o[2], o[3]);
     }
-    // where the rows cannot be moved by a tensor map: a warp brings its own 16 rows, w of them
-    __device__ __forceinline__ void bring(const void *src, int64_t ts, int tile, int w, int cb, const LinrecParams &p) {
+    // where the rows cannot be moved by a tensor map: a warp brings its own
+    __device__ __forceinline__ void bring(const void *src, int64_t ts, int tile, int wid, int cb, const LinrecParams &p) {
         const int lane = threadIdx.x & 31, c = cb * LR_CH + lane;
 #pragma unroll 4
-        for (int r = w * LR_WROWS; r < (w + 1) * LR_WROWS; ++r) {
+        for (int r = wid * (ROWS / LR_WARPS); r < (wid + 1) * (ROWS / LR_WARPS); ++r) {
             const int row = tile * ROWS + r;
             T x = to_out_t<T>(0.f);
             if (row < p.rows && c < p.dim) x = reinterpret_cast<const T *>(src)[(int64_t)row * ts + c];
@@ -262,21 +314,24 @@ template <bool V> struct Const {
     static constexpr bool value = V;
 };
 
-// Two neighbouring values of a row; VEC: they lie in one aligned piece.
-template <bool VEC, typename T>
-__device__ __forceinline__ void put2(T *p, int64_t at, F2 v, int c, int dim) {
-    float x, y;
-    v.get(x, y);
+// Four neighbouring values of a row; VEC: they lie in one aligned piece, all of them or none.
+template <bool VEC, typename T> __device__ __forceinline__ void put4(T *p, F4 v, int c, int dim) {
+    float o[4];
+    v.lo.get(o[0], o[1]), v.hi.get(o[2], o[3]);
     if (VEC) {
-        const float o[2] = {x, y};
-        if (c < dim) store_pack<T, 2>(p + at, o);
+        if (c < dim) store_pack<T, 4>(p, o);
     } else {
-        if (c < dim) p[at] = to_out_t<T>(x);
-        if (c + 1 < dim) p[at + 1] = to_out_t<T>(y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + j < dim) p[j] = to_out_t<T>(o[j]);
     }
 }
-__device__ __forceinline__ F2 get2(const float *p, int64_t at, int c, int dim) {
-    return F2(p && c < dim ? p[at] : 0.f, p && c + 1 < dim ? p[at + 1] : 0.f);
+// Four channels of an fp32 row that may be absent (zero).
+__device__ __forceinline__ F4 row4(const float *p, int64_t row, int c, int dim) {
+    float o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = p && c + j < dim ? p[row * dim + c + j] : 0.f;
+    return make4(o[0], o[1], o[2], o[3]);
 }
 
 // Sequences without a token have no row: their last state is their first (forward), their gradients pass through
@@ -299,143 +354,137 @@ __device__ __forceinline__ void check_sequences(const LinrecParams &p) {
     if (bad) atomicOr(p.status, ST_BAD_SEQLENS);
 }
 
-// a group's map (channels ch, ch + 1) as the scan's records lie in shared memory
-__device__ __forceinline__ void put_maps(float2 *at, F2 a, F2 b) {
-    float x, y, u, v;
-    a.get(x, y);
-    b.get(u, v);
-    *reinterpret_cast<float4 *>(at) = make_float4(x, u, y, v);
+// The warps' parts of the tile's map are in shared memory: the others say so and go on, the one that needs them waits.
+__device__ __forceinline__ void totals_there(bool wait) {
+    __syncwarp();
+    if (wait) asm volatile("bar.sync 1, %0;" ::"n"(LR_THREADS) : "memory");
+    else asm volatile("bar.arrive 1, %0;" ::"n"(LR_THREADS) : "memory");
 }
 
-// ---------------------------------------------------------------- forward
-template <typename T, typename G> struct FwdStage {
-    static constexpr int ROWS = LR_FWD_WARPS * LR_WROWS;
-    Tile<G, ROWS> g;
-    Tile<T, ROWS> x;
+// What the two kernels have in common: a CTA's shared memory besides the stages.
+template <int R, int S, int W> struct LinrecSmem {
+    Maps<W> maps;
+    Peers peers;
+    float2 total[LR_CH];          // the tile's map
+    float carry[LR_CH];           // what enters the tile
+    uint64_t full[S];             // a stage's rows are there
+    Ends<R> ends[2];
 };
 
-template <typename T, typename G, bool COMP, bool VEC>
-__global__ void __launch_bounds__(32 * LR_FWD_WARPS, 2)
-    k10_fwd(const __grid_constant__ LinrecParams p, const __grid_constant__ LinrecMaps maps) {
-    using Stage = FwdStage<T, G>;
-    constexpr int W = LR_FWD_WARPS, ROWS = Stage::ROWS, S = LR_FWD_STAGES;
-    extern __shared__ __align__(128) char dynamic[];
-    Stage *stages = reinterpret_cast<Stage *>(dynamic);
-    __shared__ Sequences<ROWS> seqs[2];
-    __shared__ __align__(16) float2 agg[W][LR_CH];  // a warp's map, then that of the tile's rows before it
-    __shared__ __align__(16) Peers peers;
-    __shared__ __align__(8) uint64_t full[S];
-    __shared__ uint32_t pcut;  // bit per warp: there is a cut in the tile's rows before it
-    __shared__ float carry[LR_CH];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = lane >> 4, ch = 2 * (lane & 15);
-    const int rank = cluster_rank(), cb = blockIdx.x / p.cluster, c = cb * LR_CH + ch;
-
-    auto fetch = [&](int k) {  // VEC: one thread; else every warp
-        Stage &st = stages[k % S];
-        const int tile = k * p.cluster + rank;
-        if (VEC) {
-            mbar_expect_tx(&full[k % S], sizeof(Stage));
-            load_tile(&st.g, &maps.g, cb * LR_CH, tile * ROWS, &full[k % S]);
-            load_tile(&st.x, &maps.x, cb * LR_CH, tile * ROWS, &full[k % S]);
-        } else {
-            st.g.bring(p.g, p.g_ts, tile, wid, cb, p);
-            st.x.bring(p.x, p.x_ts, tile, wid, cb, p);
-            __syncwarp();
-        }
-    };
+__device__ __forceinline__ void init_barriers(uint64_t *full, int stages, Peers &peers) {
     if (threadIdx.x == 0) {
-        for (int q = 0; q < S; ++q) mbar_init(&full[q], 1);
+        for (int q = 0; q < stages; ++q) mbar_init(&full[q], 1);
         mbar_init(&peers.bar[0], 1);
         mbar_init(&peers.bar[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+}
+
+// ---------------------------------------------------------------- forward
+template <typename T, typename G> struct FwdStages {
+    static constexpr int ROWS = LR_FWD_R * LR_GROUPS, S = 2;
+    static constexpr uint32_t BYTES = sizeof(Tile<G, ROWS>) + sizeof(Tile<T, ROWS>);
+    Tile<G, ROWS> g[S];
+    Tile<T, ROWS> x[S];
+};
+
+template <typename T, typename G, bool COMP, bool VEC>
+__global__ void __launch_bounds__(LR_THREADS, 2)
+    k10_fwd(const __grid_constant__ LinrecParams p, const __grid_constant__ LinrecMaps maps) {
+    using Stages = FwdStages<T, G>;
+    constexpr int R = LR_FWD_R, ROWS = Stages::ROWS, S = Stages::S;
+    extern __shared__ __align__(128) char dynamic[];
+    Stages &st = *reinterpret_cast<Stages *>(dynamic);
+    __shared__ __align__(16) LinrecSmem<R, S, LR_GROUPS> sm;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = threadIdx.x >> 3, ch = 4 * (lane & 7);
+    const int rank = cluster_rank(), cb = blockIdx.x / p.cluster, c = cb * LR_CH + ch;
+    const bool channels = VEC && (cb + 1) * LR_CH <= p.dim;
+
+    auto fetch = [&](int k) {  // VEC: one thread; else every warp
+        const int tile = k * p.cluster + rank;
+        if (VEC) {
+            mbar_expect_tx(&sm.full[k % S], Stages::BYTES);
+            load_tile(&st.g[k % S], &maps.g, cb * LR_CH, tile * ROWS, &sm.full[k % S]);
+            load_tile(&st.x[k % S], &maps.x, cb * LR_CH, tile * ROWS, &sm.full[k % S]);
+        } else {
+            st.g[k % S].bring(p.g, p.g_ts, tile, wid, cb, p);
+            st.x[k % S].bring(p.x, p.x_ts, tile, wid, cb, p);
+            __syncwarp();
+        }
+    };
+    init_barriers(sm.full, S, sm.peers);
     check_sequences(p);
-    if (wid == 2) seqs[0].find(p, rank);
+    int sa = 0, sb = 0;  // (warp 2) the sequence met last
+    if (wid == 2) sm.ends[0].find(p, rank, sa, sb);
     cluster_sync();  // the barriers are there, everywhere
     for (int k = 0; k < S && k < p.supers; ++k)
         if (!VEC || threadIdx.x == 0) fetch(k);
     float walked = 0.f;  // (warp 1) the state that enters the cluster's rows
     for (int k = 0; k < p.supers; ++k) {
-        const int buf = k & 1, tile = k * p.cluster + rank, first = wid * LR_WROWS + 8 * group, row0 = tile * ROWS + first;
-        const Sequences<ROWS> &sq = seqs[buf];
-        const Stage &st = stages[k % S];
-        const uint32_t wheads = sq.heads(wid), heads = wheads >> (8 * group) & 0xff;
-        const uint32_t wtails = sq.tails(wid), tails = wtails >> (8 * group) & 0xff;
-        // most warps: every row and channel is there, and no sequence starts or ends among the rows
-        const bool plain = VEC && !(wheads | wtails) && tile * ROWS + (wid + 1) * LR_WROWS <= p.rows &&
-                           (cb + 1) * LR_CH <= p.dim;
-        if (VEC) wait_phase(&full[k % S], (k / S) & 1, p);
-        F2 a[8], b[8], A, B;
+        const int buf = k & 1, tile = k * p.cluster + rank, first = group * R, row0 = tile * ROWS + first;
+        const Ends<R> &ends = sm.ends[buf];
+        const auto &gt = st.g[k % S];
+        const auto &xt = st.x[k % S];
+        const uint32_t cuts = ends.head_cuts(), heads = ends.heads(group), tails = ends.tails(group);
+        // as a rule every row and channel is there, and no sequence starts or ends among the warp's rows
+        const bool plain = channels && (tile + 1) * ROWS <= p.rows && !__any_sync(0xffffffffu, heads | tails);
+        if (VEC) wait_phase(&sm.full[k % S], (k / S) & 1, p);
+        F4 a[R], b[R], A, B;
         auto compose = [&](auto any) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                float g0, g1;
-                st.g.get(first + r, ch, g0, g1);
-                F2 rest;
-                decay2(g0, g1, a[r], rest);
-                b[r] = st.x.get(first + r, ch);
-                if (COMP) b[r] = mul2(b[r], rest);
+            for (int r = 0; r < R; ++r) {
+                float g[4];
+                gt.get(first + r, ch, g);
+                F4 rest;
+                decay2(g[0], g[1], a[r].lo, rest.lo);
+                decay2(g[2], g[3], a[r].hi, rest.hi);
+                b[r] = xt.get(first + r, ch);
+                if (COMP) b[r] = mul4(b[r], rest);
                 if (any.value && (heads >> r) & 1) {
-                    b[r] = fma2(a[r], get2(p.h0, (int64_t)sq.seq[first + r] * p.dim + c, c, p.dim), b[r]);
+                    b[r] = fma4(a[r], row4(p.h0, ends.sequence_of(p, row0 + r), c, p.dim), b[r]);
                     B = b[r];
                 } else {
-                    B = r == 0 ? b[r] : fma2(a[r], B, b[r]);
+                    B = r == 0 ? b[r] : fma4(a[r], B, b[r]);
                 }
-                A = r == 0 ? a[r] : mul2(A, a[r]);
+                A = r == 0 ? a[r] : mul4(A, a[r]);
             }
         };
         if (plain) compose(Const<false>());
         else compose(Const<true>());
-        // the first group's map for the lanes of the second, and the warp's map
-        const F2 A0 = shfl2(A, lane & 15), B0 = shfl2(B, lane & 15);
-        if (group) put_maps(&agg[wid][ch], mul2(A, A0), heads ? B : fma2(A, B0, B));
+        put_maps<LR_GROUPS>(sm.maps, group, ch, A, B);
         __syncthreads();
-        // the tile's rows are in registers: their place takes the tile after next
-        if (k + S < p.supers && (!VEC || threadIdx.x == 96)) fetch(k + S);
-        if (wid == 0) {
-            Map m;
-            uint32_t pc = 0;
-#pragma unroll 4
-            for (int w = 0; w < W; ++w) {
-                const float2 v = agg[w][lane];
-                agg[w][lane] = make_float2(m.a, m.b);
-                pc |= (uint32_t)m.cut << w;
-                m.then(v.x, v.y, sq.heads(w) != 0);
-            }
-            if (lane == 0) pcut = pc;
-            peers.tell(buf, rank, p.cluster, m);
-        } else if (wid == 1) {
-            carry[lane] = walked;
+        // the tile's rows are in registers: their place takes the tile S further on
+        if (k + S < p.supers && (!VEC || threadIdx.x == 128)) fetch(k + S);
+        scan_maps<LR_GROUPS, false>(sm.maps, cuts, wid, lane, sm.total);
+        totals_there(wid == 1);
+        if (wid == 1) {
+            sm.peers.tell(buf, rank, p.cluster, sm.total[lane], cuts != 0);
+            wait_peers(&sm.peers.bar[buf], (k >> 1) & 1, p);
+            sm.carry[lane] = sm.peers.entry(buf, rank, p.cluster, walked);
         } else if (wid == 2) {
-            if (k + 1 < p.supers) seqs[buf ^ 1].find(p, tile + p.cluster);
+            if (k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile + p.cluster, sa, sb);
             empty_sequences(p, tile, cb, p.h0, p.ht);
         }
         __syncthreads();
-        wait_peers(&peers.bar[buf], (k >> 1) & 1, p);
-        if (wid == 1) walked = peers.through(buf, p.cluster, walked);
-        F2 h = peers.entry(buf, rank, ch, F2(carry[ch], carry[ch + 1]));
-        {
-            const float4 m = *reinterpret_cast<const float4 *>(&agg[wid][ch]);
-            h = (pcut >> wid) & 1 ? F2(m.y, m.w) : fma2(F2(m.x, m.z), h, F2(m.y, m.w));
-        }
-        if (p.states && wid % LR_BWD_WARPS == 0 && group == 0 && row0 < p.rows)
-            put2<VEC>(p.states, (int64_t)(row0 / LR_TILE) * p.dim + c, h, c, p.dim);
-        if (group) h = wheads & 0xff ? B0 : fma2(A0, h, B0);
+        F4 h = through<LR_GROUPS>(sm.maps, group, ch, cuts & ((1u << group) - 1), sm.carry);
+        if (p.states && first % LR_SAVE == 0 && row0 < p.rows)
+            put4<VEC>(p.states + (int64_t)(row0 / LR_SAVE) * p.dim + c, h, c, p.dim);
         T *to = reinterpret_cast<T *>(p.h) + (int64_t)row0 * p.dim + c;
         if (plain && p.h) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                h = fma2(a[r], h, b[r]);
-                put2<true>(to, 0, h, 0, 1);
+            for (int r = 0; r < R; ++r) {
+                h = fma4(a[r], h, b[r]);
+                put4<true>(to, h, 0, 1);
                 to += p.dim;
             }
         } else {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                h = (heads >> r) & 1 ? b[r] : fma2(a[r], h, b[r]);
+            for (int r = 0; r < R; ++r) {
+                h = (heads >> r) & 1 ? b[r] : fma4(a[r], h, b[r]);
                 if (row0 + r < p.rows) {
-                    if (p.h) put2<VEC>(to, (int64_t)r * p.dim, h, c, p.dim);
-                    if (p.ht && (tails >> r) & 1) put2<VEC>(p.ht, (int64_t)sq.seq[first + r] * p.dim + c, h, c, p.dim);
+                    if (p.h) put4<VEC>(to + (int64_t)r * p.dim, h, c, p.dim);
+                    if (p.ht && (tails >> r) & 1)
+                        put4<VEC>(p.ht + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, h, c, p.dim);
                 }
             }
         }
@@ -444,168 +493,154 @@ __global__ void __launch_bounds__(32 * LR_FWD_WARPS, 2)
 }
 
 // ---------------------------------------------------------------- backward
-template <typename T, typename G> struct BwdStage {
-    static constexpr int ROWS = LR_TILE;
-    Tile<G, ROWS> g;
-    Tile<T, ROWS> x, dh;
+// g is done with when the groups' maps are formed, x and dh are read again to finish a tile: they take one place more.
+template <typename T, typename G> struct BwdStages {
+    static constexpr int ROWS = LR_BWD_R * LR_GROUPS, GS = 2, XS = 3;
+    static constexpr uint32_t BYTES = sizeof(Tile<G, ROWS>) + 2 * sizeof(Tile<T, ROWS>);
+    Tile<G, ROWS> g[GS];
+    Tile<T, ROWS> x[XS], dh[XS];
 };
 
 template <typename T, typename G, bool COMP, bool VEC>
-__global__ void __launch_bounds__(32 * LR_BWD_WARPS, 2)
+__global__ void __launch_bounds__(LR_THREADS, 2)
     k10_bwd(const __grid_constant__ LinrecParams p, const __grid_constant__ LinrecMaps maps) {
-    using Stage = BwdStage<T, G>;
-    constexpr int W = LR_BWD_WARPS, ROWS = Stage::ROWS, S = LR_BWD_STAGES;
+    using Stages = BwdStages<T, G>;
+    constexpr int R = LR_BWD_R, ROWS = Stages::ROWS, GS = Stages::GS, S = Stages::XS;
     extern __shared__ __align__(128) char dynamic[];
-    Stage *stages = reinterpret_cast<Stage *>(dynamic);
-    __shared__ Sequences<ROWS> seqs[2];
-    __shared__ __align__(16) float2 agg[W][LR_CH], fwd[W][LR_CH];  // a warp's maps, backward and forward
-    __shared__ __align__(16) Peers peers;
-    __shared__ __align__(8) uint64_t full[S];
-    __shared__ __align__(8) float entry[W][LR_CH];  // the h that enters a warp's rows
-    __shared__ uint32_t scut;                       // bit per warp: there is a cut in the tile's rows behind it
-    __shared__ __align__(8) float carry[LR_CH];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = lane >> 4, ch = 2 * (lane & 15);
+    Stages &st = *reinterpret_cast<Stages *>(dynamic);
+    __shared__ __align__(16) LinrecSmem<R, S, LR_WARPS> sm;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = threadIdx.x >> 3, ch = 4 * (lane & 7);
     const int rank = cluster_rank(), cb = blockIdx.x / p.cluster, c = cb * LR_CH + ch;
+    const bool channels = VEC && (cb + 1) * LR_CH <= p.dim;
 
     // the scan goes from the last rows to the first, in the cluster too
     auto tile_of = [&](int k) { return (p.supers - k) * p.cluster - 1 - rank; };
     auto fetch = [&](int k) {
-        Stage &st = stages[k % S];
         const int tile = tile_of(k);
         if (VEC) {
-            mbar_expect_tx(&full[k % S], sizeof(Stage));
-            load_tile(&st.g, &maps.g, cb * LR_CH, tile * ROWS, &full[k % S]);
-            load_tile(&st.x, &maps.x, cb * LR_CH, tile * ROWS, &full[k % S]);
-            load_tile(&st.dh, &maps.dh, cb * LR_CH, tile * ROWS, &full[k % S]);
+            mbar_expect_tx(&sm.full[k % S], Stages::BYTES);
+            load_tile(&st.g[k % GS], &maps.g, cb * LR_CH, tile * ROWS, &sm.full[k % S]);
+            load_tile(&st.x[k % S], &maps.x, cb * LR_CH, tile * ROWS, &sm.full[k % S]);
+            load_tile(&st.dh[k % S], &maps.dh, cb * LR_CH, tile * ROWS, &sm.full[k % S]);
         } else {
-            st.g.bring(p.g, p.g_ts, tile, wid, cb, p);
-            st.x.bring(p.x, p.x_ts, tile, wid, cb, p);
-            st.dh.bring(p.dh, p.dh_ts, tile, wid, cb, p);
+            st.g[k % GS].bring(p.g, p.g_ts, tile, wid, cb, p);
+            st.x[k % S].bring(p.x, p.x_ts, tile, wid, cb, p);
+            st.dh[k % S].bring(p.dh, p.dh_ts, tile, wid, cb, p);
             __syncwarp();
         }
     };
-    if (threadIdx.x == 0) {
-        for (int q = 0; q < S; ++q) mbar_init(&full[q], 1);
-        mbar_init(&peers.bar[0], 1);
-        mbar_init(&peers.bar[1], 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
+    init_barriers(sm.full, S, sm.peers);
     check_sequences(p);
-    if (wid == 2) seqs[0].find(p, tile_of(0));
+    int sa = 0, sb = 0;
+    if (wid == 2) sm.ends[0].find(p, tile_of(0), sa, sb);
     cluster_sync();
-    for (int k = 0; k < S - 1 && k < p.supers; ++k)
+    for (int k = 0; k < 2 && k < p.supers; ++k)
         if (!VEC || threadIdx.x == 0) fetch(k);
     float walked = 0.f;
     for (int k = 0; k < p.supers; ++k) {
-        const int buf = k & 1, tile = tile_of(k), first = wid * LR_WROWS + 8 * group, row0 = tile * ROWS + first;
-        const Sequences<ROWS> &sq = seqs[buf];
-        const Stage &st = stages[k % S];
-        const uint32_t wheads = sq.heads(wid), heads = wheads >> (8 * group) & 0xff;
-        const uint32_t wtails = sq.tails(wid), tails = wtails >> (8 * group) & 0xff;
-        const bool plain = VEC && !(wheads | wtails) && tile * ROWS + (wid + 1) * LR_WROWS <= p.rows &&
-                           (cb + 1) * LR_CH <= p.dim;
+        const int buf = k & 1, tile = tile_of(k), first = group * R, row0 = tile * ROWS + first;
+        const Ends<R> &ends = sm.ends[buf];
+        const auto &gt = st.g[k % GS];
+        const auto &xt = st.x[k % S], &dt = st.dh[k % S];
+        const uint32_t tcuts = ends.tail_cuts(), heads = ends.heads(group), tails = ends.tails(group);
+        const bool plain = channels && (tile + 1) * ROWS <= p.rows && !__any_sync(0xffffffffu, heads | tails);
+        const int warp0 = tile * ROWS + wid * LR_SAVE;  // the warp's first row
+        F4 h;                                           // enters it
+        if (plain) h = make4(*reinterpret_cast<const float4 *>(p.states + (int64_t)(warp0 / LR_SAVE) * p.dim + c));
+        else h = row4(warp0 < p.rows ? p.states : nullptr, warp0 / LR_SAVE, c, p.dim);
+        if (VEC) wait_phase(&sm.full[k % S], (k / S) & 1, p);
         auto dh_at = [&](int r, auto any) {  // with the gradient of the last state on a sequence's last row
-            F2 d = st.dh.get(first + r, ch);
-            if (any.value && (tails >> r) & 1)
-                d = add2(d, get2(p.dht, (int64_t)sq.seq[first + r] * p.dim + c, c, p.dim));
+            F4 d = dt.get(first + r, ch);
+            if (any.value && (tails >> r) & 1) d = add4(d, row4(p.dht, ends.sequence_of(p, row0 + r), c, p.dim));
             return d;
         };
-        if (VEC) wait_phase(&full[k % S], (k / S) & 1, p);
-        F2 a[8], rest[COMP ? 8 : 1], A, B, R;  // B, R: of the forward and the backward map
+        F4 a[R], rest[COMP ? R : 1], A, B, Q;  // B, Q: of the group's forward and backward map
         auto compose = [&](auto any) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                float g0, g1;
-                st.g.get(first + r, ch, g0, g1);
-                F2 u;
-                decay2(g0, g1, a[r], u);
-                F2 b = st.x.get(first + r, ch);
-                if (COMP) rest[r] = u, b = mul2(b, u);
-                if (any.value && (heads >> r) & 1)
-                    B = fma2(a[r], get2(p.h0, (int64_t)sq.seq[first + r] * p.dim + c, c, p.dim), b);
-                else B = r == 0 ? b : fma2(a[r], B, b);
-                A = r == 0 ? a[r] : mul2(A, a[r]);
+            for (int r = 0; r < R; ++r) {
+                float g[4];
+                gt.get(first + r, ch, g);
+                F4 u;
+                decay2(g[0], g[1], a[r].lo, u.lo);
+                decay2(g[2], g[3], a[r].hi, u.hi);
+                F4 b = xt.get(first + r, ch);
+                if (COMP) rest[r] = u, b = mul4(b, u);
+                if (any.value && (heads >> r) & 1) B = fma4(a[r], row4(p.h0, ends.sequence_of(p, row0 + r), c, p.dim), b);
+                else B = r == 0 ? b : fma4(a[r], B, b);
+                A = r == 0 ? a[r] : mul4(A, a[r]);
             }
 #pragma unroll
-            for (int r = 7; r >= 0; --r) {
-                const F2 d = dh_at(r, any);
-                R = mul2(a[r], r == 7 || (any.value && (tails >> r) & 1) ? d : add2(d, R));
+            for (int r = R - 1; r >= 0; --r) {
+                const F4 d = dh_at(r, any);
+                Q = mul4(a[r], r == R - 1 || (any.value && (tails >> r) & 1) ? d : add4(d, Q));
             }
         };
         if (plain) compose(Const<false>());
         else compose(Const<true>());
-        // forward: the first group's map for the lanes of the second; backward: the second's for those of the first
-        const F2 A0 = shfl2(A, lane & 15), B0 = shfl2(B, lane & 15), A1 = shfl2(A, lane | 16), R1 = shfl2(R, lane | 16);
-        if (group) put_maps(&fwd[wid][ch], mul2(A, A0), heads ? B : fma2(A, B0, B));
-        else put_maps(&agg[wid][ch], mul2(A, A1), tails ? R : fma2(A, R1, R));
+        // backward: the maps of the groups from this one to the warp's last, for the warp's map and what enters the groups
+        const int q = lane >> 3;
+        const uint32_t cut_from = __ballot_sync(0xffffffffu, tails) >> lane;  // bit 8 i: the group i further on cuts off
+        F4 AQ = A, QQ = Q;
+#pragma unroll
+        for (int d = 1; d < 4; d *= 2) {
+            const F4 A1 = shfl4(AQ, (lane + 8 * d) & 31), Q1 = shfl4(QQ, (lane + 8 * d) & 31);
+            if (q + d < 4) {
+                if (!(cut_from & (d == 1 ? 1u : 0x101u))) QQ = fma4(AQ, Q1, QQ);
+                AQ = mul4(AQ, A1);
+            }
+        }
+        if (q == 0) put_maps<LR_WARPS>(sm.maps, wid, ch, AQ, QQ);
+        // forward: what enters the warp's groups, one after the other
+#pragma unroll
+        for (int d = 1; d < 4; ++d) {
+            const F4 out = shfl4(heads ? B : fma4(A, h, B), (lane - 8) & 31);
+            if (q == d) h = out;
+        }
         __syncthreads();
-        // everybody is done with the tile before: its place takes the one S - 1 further on
-        if (k + S - 1 < p.supers && (!VEC || threadIdx.x == 96)) fetch(k + S - 1);
-        if (wid == 0) {
-            Map m;
-            uint32_t sc = 0;
-#pragma unroll 4
-            for (int w = W - 1; w >= 0; --w) {
-                const float2 v = agg[w][lane];
-                agg[w][lane] = make_float2(m.a, m.b);
-                sc |= (uint32_t)m.cut << w;
-                m.then(v.x, v.y, sq.tails(w) != 0);
-            }
-            if (lane == 0) scut = sc;
-            peers.tell(buf, rank, p.cluster, m);
-        } else if (wid == 1) {
-            carry[lane] = walked;
-            const int col = cb * LR_CH + lane;
-            float h = !(sq.head[0] & 1) && tile > 0 && tile < p.tiles && col < p.dim ? p.states[(size_t)tile * p.dim + col] : 0.f;
-#pragma unroll 4
-            for (int w = 0; w < W; ++w) {
-                entry[w][lane] = h;
-                const float2 v = fwd[w][lane];
-                h = sq.heads(w) ? v.y : fmaf(v.x, h, v.y);
-            }
+        // everybody is done with this tile's g and with the tile before: their places take the tile after next
+        if (k + 2 < p.supers && (!VEC || threadIdx.x == 128)) fetch(k + 2);
+        scan_maps<LR_WARPS, true>(sm.maps, tcuts, wid, lane, sm.total);
+        totals_there(wid == 1);
+        if (wid == 1) {
+            sm.peers.tell(buf, rank, p.cluster, sm.total[lane], tcuts != 0);
+            wait_peers(&sm.peers.bar[buf], (k >> 1) & 1, p);
+            sm.carry[lane] = sm.peers.entry(buf, rank, p.cluster, walked);
         } else if (wid == 2) {
-            if (k + 1 < p.supers) seqs[buf ^ 1].find(p, tile - p.cluster);
+            if (k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile - p.cluster, sa, sb);
             empty_sequences(p, tile, cb, p.dht, p.dh0);
         }
         __syncthreads();
-        // the part that does not need what enters backwards: h_{t-1} of every row, less x_t with COMP
-        F2 h(entry[wid][ch], entry[wid][ch + 1]), before[8];
-        if (group) h = wheads & 0xff ? B0 : fma2(A0, h, B0);
-        auto recompute = [&](auto any) {
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                if (any.value && (heads >> r) & 1) h = get2(p.h0, (int64_t)sq.seq[first + r] * p.dim + c, c, p.dim);
-                const F2 x = st.x.get(first + r, ch);
-                before[r] = COMP ? fma2(x, F2(-1.f), h) : h;
-                h = fma2(a[r], h, COMP ? mul2(x, rest[r]) : x);
-            }
-        };
-        if (plain) recompute(Const<false>());
-        else recompute(Const<true>());
-        wait_peers(&peers.bar[buf], (k >> 1) & 1, p);
-        if (wid == 1) walked = peers.through(buf, p.cluster, walked);
-        F2 m = peers.entry(buf, rank, ch, F2(carry[ch], carry[ch + 1]));
+        F4 m = through<LR_WARPS>(sm.maps, wid, ch, tcuts & ((1u << (LR_WARPS - 1 - wid)) - 1), sm.carry);
         {
-            const float4 q = *reinterpret_cast<const float4 *>(&agg[wid][ch]);
-            m = (scut >> wid) & 1 ? F2(q.y, q.w) : fma2(F2(q.x, q.z), m, F2(q.y, q.w));
+            // from the warp's end to the group's: through the maps of the groups behind it
+            const F4 A1 = shfl4(AQ, (lane + 8) & 31), Q1 = shfl4(QQ, (lane + 8) & 31);
+            if (q < 3) m = cut_from & 0x01010100u ? Q1 : fma4(A1, m, Q1);
         }
-        if (!group) m = wtails >> 8 ? R1 : fma2(A1, m, R1);
         auto finish = [&](auto any) {
-            const int64_t end = (int64_t)(row0 + 7) * p.dim + c;
+            F4 before[R];  // h_{t-1}, less x_t with COMP
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (any.value && (heads >> r) & 1) h = row4(p.h0, ends.sequence_of(p, row0 + r), c, p.dim);
+                const F4 x = xt.get(first + r, ch);
+                const F2 minus(-1.f);
+                before[r] = COMP ? fma4(x, F4{minus, minus}, h) : h;
+                h = fma4(a[r], h, COMP ? mul4(x, rest[r]) : x);
+            }
+            const int64_t end = (int64_t)(row0 + R - 1) * p.dim + c;
             T *dx = reinterpret_cast<T *>(p.dx) + end;
             G *dg = reinterpret_cast<G *>(p.dg) + end;
 #pragma unroll
-            for (int r = 7; r >= 0; --r) {
-                const F2 d = dh_at(r, any), lam = any.value && (tails >> r) & 1 ? d : add2(d, m);
-                m = mul2(a[r], lam);
+            for (int r = R - 1; r >= 0; --r) {
+                const F4 d = dh_at(r, any), lam = any.value && (tails >> r) & 1 ? d : add4(d, m);
+                m = mul4(a[r], lam);
                 if (!any.value) {
-                    put2<true>(dx, 0, COMP ? mul2(rest[r], lam) : lam, 0, 1);
-                    put2<true>(dg, 0, mul2(m, before[r]), 0, 1);
+                    put4<true>(dx, COMP ? mul4(rest[r], lam) : lam, 0, 1);
+                    put4<true>(dg, mul4(m, before[r]), 0, 1);
                 } else if (row0 + r < p.rows) {
-                    put2<VEC>(dx, 0, COMP ? mul2(rest[r], lam) : lam, c, p.dim);
-                    put2<VEC>(dg, 0, mul2(m, before[r]), c, p.dim);
+                    put4<VEC>(dx, COMP ? mul4(rest[r], lam) : lam, c, p.dim);
+                    put4<VEC>(dg, mul4(m, before[r]), c, p.dim);
                     if (p.dh0 && (heads >> r) & 1)
-                        put2<VEC>(p.dh0, (int64_t)sq.seq[first + r] * p.dim + c, m, c, p.dim);
+                        put4<VEC>(p.dh0 + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, m, c, p.dim);
                 }
                 dx -= p.dim, dg -= p.dim;
             }
@@ -648,32 +683,31 @@ template <typename T, typename G, int V, bool COMP> __global__ void __launch_bou
 
 }  // namespace
 
-#define RUN(KERNEL, STAGE, STAGES, THREADS)                                                         \
+#define RUN(KERNEL, STAGES)                                                                         \
     do {                                                                                            \
-        constexpr int smem = (int)sizeof(STAGE) * STAGES;                                           \
-        LinrecLaunch l((const void *)KERNEL, THREADS, smem);                                        \
-        cudaError_t e = linrec_plan(p, l, STAGE::ROWS, stream);                                     \
+        LinrecLaunch l((const void *)KERNEL, LR_THREADS, (int)sizeof(STAGES));                      \
+        cudaError_t e = linrec_plan(p, l, STAGES::ROWS, stream);                                    \
         LinrecMaps maps;                                                                            \
-        if (e == cudaSuccess && p.vec) e = linrec_maps(p, maps, STAGE::ROWS);                       \
+        if (e == cudaSuccess && p.vec) e = linrec_maps(p, maps, STAGES::ROWS);                      \
         if (e != cudaSuccess) return e;                                                             \
         return cudaLaunchKernelEx(&l.cfg, KERNEL, static_cast<const LinrecParams>(p), static_cast<const LinrecMaps>(maps)); \
     } while (0)
-#define RUN_ALL(KERNEL, STAGE, STAGES, THREADS)                                                     \
+#define RUN_ALL(KERNEL, STAGES)                                                                     \
     do {                                                                                            \
-        using Stage = STAGE;                                                                        \
-        if (p.vec && p.complement) RUN((KERNEL<T, G, true, true>), Stage, STAGES, THREADS);         \
-        if (p.vec) RUN((KERNEL<T, G, false, true>), Stage, STAGES, THREADS);                        \
-        if (p.complement) RUN((KERNEL<T, G, true, false>), Stage, STAGES, THREADS);                 \
-        RUN((KERNEL<T, G, false, false>), Stage, STAGES, THREADS);                                  \
+        using Stages = STAGES;                                                                      \
+        if (p.vec && p.complement) RUN((KERNEL<T, G, true, true>), Stages);                         \
+        if (p.vec) RUN((KERNEL<T, G, false, true>), Stages);                                        \
+        if (p.complement) RUN((KERNEL<T, G, true, false>), Stages);                                 \
+        RUN((KERNEL<T, G, false, false>), Stages);                                                  \
     } while (0)
 
 template <typename T, typename G> cudaError_t linrec_fwd_t(LinrecParams &p, cudaStream_t stream) {
-    using FS = FwdStage<T, G>;
-    RUN_ALL(k10_fwd, FS, LR_FWD_STAGES, 32 * LR_FWD_WARPS);
+    using FS = FwdStages<T, G>;
+    RUN_ALL(k10_fwd, FS);
 }
 template <typename T, typename G> cudaError_t linrec_bwd_t(LinrecParams &p, cudaStream_t stream) {
-    using BS = BwdStage<T, G>;
-    RUN_ALL(k10_bwd, BS, LR_BWD_STAGES, 32 * LR_BWD_WARPS);
+    using BS = BwdStages<T, G>;
+    RUN_ALL(k10_bwd, BS);
 }
 #undef RUN
 #undef RUN_ALL

@@ -96,13 +96,12 @@ size_t gdr_norm_workspace_bytes(int64_t rows, int64_t dim, int sums);
  * h0, ht [N, dim] fp32: the state before the first and after the last token of each sequence, h0 NULL means
  * zero, ht NULL not returned.  N = batch, or num_seqs when > 0 (varlen: batch 1, cu_seqlens as in gdr_bwd.h;
  * empty sequences give ht = h0).  batch * tokens is at most 2^30.
- * states, if not NULL: fp32 [ceil(batch tokens / GDR_LINREC_TILE), dim], the state that enters each tile of
- * GDR_LINREC_TILE rows (of no meaning where a sequence starts on the tile's first row); the backward takes
- * them.  h may be NULL (states and ht alone).
+ * states, if not NULL: fp32 [ceil(batch tokens / GDR_LINREC_SAVE), dim], the state that enters each GDR_LINREC_SAVE
+ * rows (of no meaning where a sequence starts on the first of them); the backward takes them.  h may be NULL (states and ht alone).
  * workspace: gdr_linrec_workspace_bytes(batch * tokens, dim) bytes, 256-byte aligned, not used by another call
  * that may run at the same time.  Malformed cu_seqlens and waits that expire are read with
  * gdr_linrec_get_status. */
-#define GDR_LINREC_TILE 128
+#define GDR_LINREC_SAVE 16
 typedef struct {
     const void *x, *g;
     const float *h0;
