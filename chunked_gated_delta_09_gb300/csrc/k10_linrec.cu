@@ -7,9 +7,9 @@
 namespace gdr {
 namespace {
 
-// For clusters of 1, 2, 4, 8 and 16 CTAs: how many clusters of a kernel the device holds at a time (0: none).
+// For clusters of 1 to 16 CTAs: how many clusters of a kernel the device holds at a time (0: none).
 struct Resident {
-    int clusters[5];
+    int clusters[LR_MAX_CLUSTER + 1];
 };
 std::mutex g_mu;
 std::unordered_map<const void *, Resident> g_resident[64];  // per device
@@ -28,15 +28,15 @@ cudaError_t resident(LinrecLaunch &l, Resident &out) {
     }
     if ((e = cudaFuncSetAttribute(l.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, l.smem)) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(l.kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-    for (int k = 0; k < 5; ++k) {
-        l.cfg.gridDim = dim3(16);
-        l.attr.val.clusterDim.x = 1u << k;
-        if (cudaOccupancyMaxActiveClusters(&out.clusters[k], l.kernel, &l.cfg) != cudaSuccess) {
+    for (int size = 1; size <= LR_MAX_CLUSTER; ++size) {
+        l.cfg.gridDim = dim3((unsigned)size);
+        l.attr.val.clusterDim.x = (unsigned)size;
+        if (cudaOccupancyMaxActiveClusters(&out.clusters[size], l.kernel, &l.cfg) != cudaSuccess) {
             cudaGetLastError();
-            out.clusters[k] = 0;
+            out.clusters[size] = 0;
         }
     }
-    if (out.clusters[0] < 1) return cudaErrorInvalidConfiguration;
+    if (out.clusters[1] < 1) return cudaErrorInvalidConfiguration;
     if (dev >= 0 && dev < 64) g_resident[dev][l.kernel] = out;
     return cudaSuccess;
 }
@@ -62,10 +62,10 @@ cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, cud
     // the size whose clusters take the fewest tiles one after the other, all waves of them together; of equal ones the
     // smallest
     int64_t best = -1;
-    for (int k = 0; k < 5; ++k) {
-        const int size = 1 << k;
-        if (r.clusters[k] < 1 || (k > 0 && size / 2 >= p.tiles)) continue;
-        const int64_t waves = (nblk + r.clusters[k] - 1) / r.clusters[k], turns = waves * ((p.tiles + size - 1) / size);
+    for (int size = 1; size <= LR_MAX_CLUSTER; ++size) {
+        if (r.clusters[size] < 1 || size > p.tiles) continue;
+        const int64_t waves = (nblk + r.clusters[size] - 1) / r.clusters[size];
+        const int64_t turns = waves * ((p.tiles + size - 1) / size);
         if (best < 0 || turns < best) best = turns, p.cluster = size;
     }
     if (const char *w = getenv("LR_CLUSTER")) p.cluster = atoi(w);

@@ -8,7 +8,7 @@
 // came before it (a flag rather than A = 0, so that a nan does not pass from one sequence to the next).
 //
 // A cluster of CTAs owns a block of 32 channels and goes through all rows, a tile for each CTA at a time.  Eight lanes
-// with four channels each compose a group of 8 (backwards 4) rows and keep a and b in registers; the groups' maps are
+// with four channels each (backwards 16 with two) compose a group of 8 rows and keep a and b in registers; the groups' maps are
 // composed by warp scans over shared memory, and the tile's map is sent to every CTA of the cluster, which then knows
 // the state that enters its own tile and finishes its rows.  So every value is read once and written once, nothing is
 // exchanged through memory, and the order of all sums is fixed: results are bit-identical from run to run.  The next
@@ -27,9 +27,9 @@ using tc::mbar_init;
 using tc::mbar_wait;
 
 constexpr int LR_WARPS = 8, LR_THREADS = 32 * LR_WARPS;
-constexpr int LR_GROUPS = 32;                // of a tile, 4 to a warp
-constexpr int LR_FWD_R = 8, LR_BWD_R = 4;    // rows of a group
-static_assert(LR_SAVE == 4 * LR_BWD_R, "a saved state enters each warp's rows of the backward");
+constexpr int LR_R = 8;                        // rows of a group
+constexpr int LR_GROUPS = 32, LR_BWD_GROUPS = 16;  // groups of a tile, 4 (backwards 2) to a warp
+static_assert(LR_SAVE == LR_BWD_GROUPS / LR_WARPS * LR_R, "a saved state enters each warp's rows of the backward");
 
 // ---------------------------------------------------------------- pairs of fp32 values, one instruction for both
 struct F2 {
@@ -138,11 +138,14 @@ template <int W> __device__ __forceinline__ F4 through(const Maps<W> &maps, int 
     const F4 b = make4(m0.y, m1.y, m2.y, m3.y);
     return cut ? b : fma4(make4(m0.x, m1.x, m2.x, m3.x), make4(*reinterpret_cast<const float4 *>(s + ch)), b);
 }
-__device__ __forceinline__ F4 shfl4(F4 v, int lane) {
-    float x, y, z, w;
-    v.lo.get(x, y), v.hi.get(z, w);
-    return make4(__shfl_sync(0xffffffffu, x, lane), __shfl_sync(0xffffffffu, y, lane), __shfl_sync(0xffffffffu, z, lane),
-                 __shfl_sync(0xffffffffu, w, lane));
+__device__ __forceinline__ F2 through2(const float2 *m, bool cut, const float *s) {
+    const F2 b(m[0].y, m[1].y);
+    return cut ? b : fma2(F2(m[0].x, m[1].x), F2(s[0], s[1]), b);
+}
+__device__ __forceinline__ F2 shfl2(F2 v, int lane) {
+    float x, y;
+    v.get(x, y);
+    return F2(__shfl_sync(0xffffffffu, x, lane), __shfl_sync(0xffffffffu, y, lane));
 }
 
 __device__ __forceinline__ int cluster_rank() {
@@ -225,18 +228,18 @@ struct Peers {
 
 // ---------------------------------------------------------------- a tile's rows
 // Which rows of a tile are the first or the last of a sequence.
-template <int R> struct Ends {
-    static constexpr int ROWS = R * LR_GROUPS;
-    uint32_t head[R], tail[R];  // a bit for each row
+template <int ROWS> struct Ends {
+    static constexpr int R = LR_R;
+    uint32_t head[ROWS / 32], tail[ROWS / 32];  // a bit for each row
     // by one warp; [a, b): the sequence that the warp met last, with which it goes on
     __device__ __forceinline__ void find(const LinrecParams &p, int tile, int &a, int &b) {
         const int lane = threadIdx.x & 31, row0 = tile * ROWS, end = min(row0 + ROWS, p.rows);
         if (row0 < p.rows && !(a <= row0 && row0 < b)) sequence_of(p, row0, a, b);
         if (row0 >= p.rows || (a < row0 && b > end)) {  // the tile lies within one sequence, or has no rows
-            if (lane < R) head[lane] = tail[lane] = 0;
+            if (lane < ROWS / 32) head[lane] = tail[lane] = 0;
             return;
         }
-        for (int k = 0; k < R; ++k) {
+        for (int k = 0; k < ROWS / 32; ++k) {
             const int row = row0 + 32 * k + lane;
             int from = -1, to = -1;
             if (row < p.rows) sequence_of(p, row, from, to);
@@ -273,7 +276,7 @@ template <int R> struct Ends {
     __device__ __forceinline__ uint32_t head_cuts() const { return __ballot_sync(0xffffffffu, heads(threadIdx.x & 31)); }
     // bit per warp, from the last one on: a sequence ends among its rows
     __device__ __forceinline__ uint32_t tail_cuts() const {
-        const int w = LR_WARPS - 1 - (threadIdx.x & (LR_WARPS - 1)), n = 4 * R;
+        const int w = LR_WARPS - 1 - (threadIdx.x & (LR_WARPS - 1)), n = ROWS / LR_WARPS;
         const uint32_t e = tail[w * n / 32] >> (w * n % 32) & (n < 32 ? (1u << (n & 31)) - 1 : 0xffffffffu);
         return __ballot_sync(0xffffffffu, e) & ((1u << LR_WARPS) - 1);
     }
@@ -285,10 +288,14 @@ template <typename T, int ROWS> struct Tile {
     __device__ __forceinline__ void get(int r, int ch, float (&o)[4]) const {
         unpack<T, 4>(*reinterpret_cast<const Pack<T, 4> *>(&v[r][ch]), o);
     }
-    __device__ __forceinline__ F4 get(int r, int ch) const {
+    __device__ __forceinline__ F4 get4(int r, int ch) const {
         float o[4];
         get(r, ch, o);
         return make4(o[0], o[1], o[2], o[3]);
+    }
+    __device__ __forceinline__ F2 get2(int r, int ch) const {
+        const Pack<T, 2> q = *reinterpret_cast<const Pack<T, 2> *>(&v[r][ch]);
+        return F2(to_f32(q.v[0]), to_f32(q.v[1]));
     }
     // where the rows cannot be moved by a tensor map: a warp brings its own
     __device__ __forceinline__ void bring(const void *src, int64_t ts, int tile, int wid, int cb, const LinrecParams &p) {
@@ -326,6 +333,20 @@ template <bool VEC, typename T> __device__ __forceinline__ void put4(T *p, F4 v,
             if (c + j < dim) p[j] = to_out_t<T>(o[j]);
     }
 }
+template <bool VEC, typename T> __device__ __forceinline__ void put2(T *p, F2 v, int c, int dim) {
+    float o[2];
+    v.get(o[0], o[1]);
+    if (VEC) {
+        if (c < dim) store_pack<T, 2>(p, o);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (c + j < dim) p[j] = to_out_t<T>(o[j]);
+    }
+}
+__device__ __forceinline__ F2 row2(const float *p, int64_t row, int c, int dim) {
+    return F2(p && c < dim ? p[row * dim + c] : 0.f, p && c + 1 < dim ? p[row * dim + c + 1] : 0.f);
+}
 // Four channels of an fp32 row that may be absent (zero).
 __device__ __forceinline__ F4 row4(const float *p, int64_t row, int c, int dim) {
     float o[4];
@@ -362,13 +383,13 @@ __device__ __forceinline__ void totals_there(bool wait) {
 }
 
 // What the two kernels have in common: a CTA's shared memory besides the stages.
-template <int R, int S, int W> struct LinrecSmem {
+template <int ROWS, int S, int W> struct LinrecSmem {
     Maps<W> maps;
     Peers peers;
     float2 total[LR_CH];          // the tile's map
     float carry[LR_CH];           // what enters the tile
     uint64_t full[S];             // a stage's rows are there
-    Ends<R> ends[2];
+    Ends<ROWS> ends[2];
 };
 
 __device__ __forceinline__ void init_barriers(uint64_t *full, int stages, Peers &peers) {
@@ -382,7 +403,7 @@ __device__ __forceinline__ void init_barriers(uint64_t *full, int stages, Peers 
 
 // ---------------------------------------------------------------- forward
 template <typename T, typename G> struct FwdStages {
-    static constexpr int ROWS = LR_FWD_R * LR_GROUPS, S = 2;
+    static constexpr int ROWS = LR_R * LR_GROUPS, S = 2;
     static constexpr uint32_t BYTES = sizeof(Tile<G, ROWS>) + sizeof(Tile<T, ROWS>);
     Tile<G, ROWS> g[S];
     Tile<T, ROWS> x[S];
@@ -392,10 +413,10 @@ template <typename T, typename G, bool COMP, bool VEC>
 __global__ void __launch_bounds__(LR_THREADS, 2)
     k10_fwd(const __grid_constant__ LinrecParams p, const __grid_constant__ LinrecMaps maps) {
     using Stages = FwdStages<T, G>;
-    constexpr int R = LR_FWD_R, ROWS = Stages::ROWS, S = Stages::S;
+    constexpr int R = LR_R, ROWS = Stages::ROWS, S = Stages::S;
     extern __shared__ __align__(128) char dynamic[];
     Stages &st = *reinterpret_cast<Stages *>(dynamic);
-    __shared__ __align__(16) LinrecSmem<R, S, LR_GROUPS> sm;
+    __shared__ __align__(16) LinrecSmem<ROWS, S, LR_GROUPS> sm;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = threadIdx.x >> 3, ch = 4 * (lane & 7);
     const int rank = cluster_rank(), cb = blockIdx.x / p.cluster, c = cb * LR_CH + ch;
     const bool channels = VEC && (cb + 1) * LR_CH <= p.dim;
@@ -422,7 +443,7 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
     float walked = 0.f;  // (warp 1) the state that enters the cluster's rows
     for (int k = 0; k < p.supers; ++k) {
         const int buf = k & 1, tile = k * p.cluster + rank, first = group * R, row0 = tile * ROWS + first;
-        const Ends<R> &ends = sm.ends[buf];
+        const Ends<ROWS> &ends = sm.ends[buf];
         const auto &gt = st.g[k % S];
         const auto &xt = st.x[k % S];
         const uint32_t cuts = ends.head_cuts(), heads = ends.heads(group), tails = ends.tails(group);
@@ -438,7 +459,7 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
                 F4 rest;
                 decay2(g[0], g[1], a[r].lo, rest.lo);
                 decay2(g[2], g[3], a[r].hi, rest.hi);
-                b[r] = xt.get(first + r, ch);
+                b[r] = xt.get4(first + r, ch);
                 if (COMP) b[r] = mul4(b[r], rest);
                 if (any.value && (heads >> r) & 1) {
                     b[r] = fma4(a[r], row4(p.h0, ends.sequence_of(p, row0 + r), c, p.dim), b[r]);
@@ -495,7 +516,7 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
 // ---------------------------------------------------------------- backward
 // g is done with when the groups' maps are formed, x and dh are read again to finish a tile: they take one place more.
 template <typename T, typename G> struct BwdStages {
-    static constexpr int ROWS = LR_BWD_R * LR_GROUPS, GS = 2, XS = 3;
+    static constexpr int ROWS = LR_R * LR_BWD_GROUPS, GS = 2, XS = 3;
     static constexpr uint32_t BYTES = sizeof(Tile<G, ROWS>) + 2 * sizeof(Tile<T, ROWS>);
     Tile<G, ROWS> g[GS];
     Tile<T, ROWS> x[XS], dh[XS];
@@ -505,11 +526,11 @@ template <typename T, typename G, bool COMP, bool VEC>
 __global__ void __launch_bounds__(LR_THREADS, 2)
     k10_bwd(const __grid_constant__ LinrecParams p, const __grid_constant__ LinrecMaps maps) {
     using Stages = BwdStages<T, G>;
-    constexpr int R = LR_BWD_R, ROWS = Stages::ROWS, GS = Stages::GS, S = Stages::XS;
+    constexpr int R = LR_R, ROWS = Stages::ROWS, GS = Stages::GS, S = Stages::XS;
     extern __shared__ __align__(128) char dynamic[];
     Stages &st = *reinterpret_cast<Stages *>(dynamic);
-    __shared__ __align__(16) LinrecSmem<R, S, LR_WARPS> sm;
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = threadIdx.x >> 3, ch = 4 * (lane & 7);
+    __shared__ __align__(16) LinrecSmem<ROWS, S, LR_WARPS> sm;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = threadIdx.x >> 4, ch = 2 * (lane & 15);
     const int rank = cluster_rank(), cb = blockIdx.x / p.cluster, c = cb * LR_CH + ch;
     const bool channels = VEC && (cb + 1) * LR_CH <= p.dim;
 
@@ -539,63 +560,54 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
     float walked = 0.f;
     for (int k = 0; k < p.supers; ++k) {
         const int buf = k & 1, tile = tile_of(k), first = group * R, row0 = tile * ROWS + first;
-        const Ends<R> &ends = sm.ends[buf];
+        const Ends<ROWS> &ends = sm.ends[buf];
         const auto &gt = st.g[k % GS];
         const auto &xt = st.x[k % S], &dt = st.dh[k % S];
         const uint32_t tcuts = ends.tail_cuts(), heads = ends.heads(group), tails = ends.tails(group);
         const bool plain = channels && (tile + 1) * ROWS <= p.rows && !__any_sync(0xffffffffu, heads | tails);
         const int warp0 = tile * ROWS + wid * LR_SAVE;  // the warp's first row
-        F4 h;                                           // enters it
-        if (plain) h = make4(*reinterpret_cast<const float4 *>(p.states + (int64_t)(warp0 / LR_SAVE) * p.dim + c));
-        else h = row4(warp0 < p.rows ? p.states : nullptr, warp0 / LR_SAVE, c, p.dim);
+        // the h that enters it
+        F2 h = plain ? *reinterpret_cast<const F2 *>(p.states + (int64_t)(warp0 / LR_SAVE) * p.dim + c)
+                     : row2(warp0 < p.rows ? p.states : nullptr, warp0 / LR_SAVE, c, p.dim);
         if (VEC) wait_phase(&sm.full[k % S], (k / S) & 1, p);
         auto dh_at = [&](int r, auto any) {  // with the gradient of the last state on a sequence's last row
-            F4 d = dt.get(first + r, ch);
-            if (any.value && (tails >> r) & 1) d = add4(d, row4(p.dht, ends.sequence_of(p, row0 + r), c, p.dim));
+            F2 d = dt.get2(first + r, ch);
+            if (any.value && (tails >> r) & 1) d = add2(d, row2(p.dht, ends.sequence_of(p, row0 + r), c, p.dim));
             return d;
         };
-        F4 a[R], rest[COMP ? R : 1], A, B, Q;  // B, Q: of the group's forward and backward map
+        F2 a[R], rest[COMP ? R : 1], A, B, Q;  // B, Q: of the group's forward and backward map
         auto compose = [&](auto any) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float g[4];
-                gt.get(first + r, ch, g);
-                F4 u;
-                decay2(g[0], g[1], a[r].lo, u.lo);
-                decay2(g[2], g[3], a[r].hi, u.hi);
-                F4 b = xt.get(first + r, ch);
-                if (COMP) rest[r] = u, b = mul4(b, u);
-                if (any.value && (heads >> r) & 1) B = fma4(a[r], row4(p.h0, ends.sequence_of(p, row0 + r), c, p.dim), b);
-                else B = r == 0 ? b : fma4(a[r], B, b);
-                A = r == 0 ? a[r] : mul4(A, a[r]);
+                const Pack<G, 2> g = *reinterpret_cast<const Pack<G, 2> *>(&gt.v[first + r][ch]);
+                F2 u;
+                decay2(to_f32(g.v[0]), to_f32(g.v[1]), a[r], u);
+                F2 b = xt.get2(first + r, ch);
+                if (COMP) rest[r] = u, b = mul2(b, u);
+                if (any.value && (heads >> r) & 1) B = fma2(a[r], row2(p.h0, ends.sequence_of(p, row0 + r), c, p.dim), b);
+                else B = r == 0 ? b : fma2(a[r], B, b);
+                A = r == 0 ? a[r] : mul2(A, a[r]);
             }
 #pragma unroll
             for (int r = R - 1; r >= 0; --r) {
-                const F4 d = dh_at(r, any);
-                Q = mul4(a[r], r == R - 1 || (any.value && (tails >> r) & 1) ? d : add4(d, Q));
+                const F2 d = dh_at(r, any);
+                Q = mul2(a[r], r == R - 1 || (any.value && (tails >> r) & 1) ? d : add2(d, Q));
             }
         };
         if (plain) compose(Const<false>());
         else compose(Const<true>());
-        // backward: the maps of the groups from this one to the warp's last, for the warp's map and what enters the groups
-        const int q = lane >> 3;
-        const uint32_t cut_from = __ballot_sync(0xffffffffu, tails) >> lane;  // bit 8 i: the group i further on cuts off
-        F4 AQ = A, QQ = Q;
-#pragma unroll
-        for (int d = 1; d < 4; d *= 2) {
-            const F4 A1 = shfl4(AQ, (lane + 8 * d) & 31), Q1 = shfl4(QQ, (lane + 8 * d) & 31);
-            if (q + d < 4) {
-                if (!(cut_from & (d == 1 ? 1u : 0x101u))) QQ = fma4(AQ, Q1, QQ);
-                AQ = mul4(AQ, A1);
-            }
+        // backward: the second group's map for the lanes of the first, which leave the warp's
+        const uint32_t ended = __ballot_sync(0xffffffffu, tails);
+        const F2 A1 = shfl2(A, lane | 16), Q1 = shfl2(Q, lane | 16);
+        if (lane < 16) {
+            float x, y, u, v;
+            mul2(A, A1).get(x, y);
+            (tails ? Q : fma2(A, Q1, Q)).get(u, v);
+            sm.maps[wid][ch] = make_float2(x, u), sm.maps[wid][ch + 1] = make_float2(y, v);
         }
-        if (q == 0) put_maps<LR_WARPS>(sm.maps, wid, ch, AQ, QQ);
-        // forward: what enters the warp's groups, one after the other
-#pragma unroll
-        for (int d = 1; d < 4; ++d) {
-            const F4 out = shfl4(heads ? B : fma4(A, h, B), (lane - 8) & 31);
-            if (q == d) h = out;
-        }
+        // forward: what leaves the first group enters the second
+        const F2 out = shfl2(heads ? B : fma2(A, h, B), lane & 15);
+        if (lane >= 16) h = out;
         __syncthreads();
         // everybody is done with this tile's g and with the tile before: their places take the tile after next
         if (k + 2 < p.supers && (!VEC || threadIdx.x == 128)) fetch(k + 2);
@@ -610,37 +622,32 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
             empty_sequences(p, tile, cb, p.dht, p.dh0);
         }
         __syncthreads();
-        F4 m = through<LR_WARPS>(sm.maps, wid, ch, tcuts & ((1u << (LR_WARPS - 1 - wid)) - 1), sm.carry);
-        {
-            // from the warp's end to the group's: through the maps of the groups behind it
-            const F4 A1 = shfl4(AQ, (lane + 8) & 31), Q1 = shfl4(QQ, (lane + 8) & 31);
-            if (q < 3) m = cut_from & 0x01010100u ? Q1 : fma4(A1, m, Q1);
-        }
+        F2 m = through2(&sm.maps[wid][ch], tcuts & ((1u << (LR_WARPS - 1 - wid)) - 1), &sm.carry[ch]);
+        if (lane < 16) m = ended >> 16 ? Q1 : fma2(A1, m, Q1);
         auto finish = [&](auto any) {
-            F4 before[R];  // h_{t-1}, less x_t with COMP
+            F2 before[R];  // h_{t-1}, less x_t with COMP
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                if (any.value && (heads >> r) & 1) h = row4(p.h0, ends.sequence_of(p, row0 + r), c, p.dim);
-                const F4 x = xt.get(first + r, ch);
-                const F2 minus(-1.f);
-                before[r] = COMP ? fma4(x, F4{minus, minus}, h) : h;
-                h = fma4(a[r], h, COMP ? mul4(x, rest[r]) : x);
+                if (any.value && (heads >> r) & 1) h = row2(p.h0, ends.sequence_of(p, row0 + r), c, p.dim);
+                const F2 x = xt.get2(first + r, ch);
+                before[r] = COMP ? fma2(x, F2(-1.f), h) : h;
+                h = fma2(a[r], h, COMP ? mul2(x, rest[r]) : x);
             }
             const int64_t end = (int64_t)(row0 + R - 1) * p.dim + c;
             T *dx = reinterpret_cast<T *>(p.dx) + end;
             G *dg = reinterpret_cast<G *>(p.dg) + end;
 #pragma unroll
             for (int r = R - 1; r >= 0; --r) {
-                const F4 d = dh_at(r, any), lam = any.value && (tails >> r) & 1 ? d : add4(d, m);
-                m = mul4(a[r], lam);
+                const F2 d = dh_at(r, any), lam = any.value && (tails >> r) & 1 ? d : add2(d, m);
+                m = mul2(a[r], lam);
                 if (!any.value) {
-                    put4<true>(dx, COMP ? mul4(rest[r], lam) : lam, 0, 1);
-                    put4<true>(dg, mul4(m, before[r]), 0, 1);
+                    put2<true>(dx, COMP ? mul2(rest[r], lam) : lam, 0, 1);
+                    put2<true>(dg, mul2(m, before[r]), 0, 1);
                 } else if (row0 + r < p.rows) {
-                    put4<VEC>(dx, COMP ? mul4(rest[r], lam) : lam, c, p.dim);
-                    put4<VEC>(dg, mul4(m, before[r]), c, p.dim);
+                    put2<VEC>(dx, COMP ? mul2(rest[r], lam) : lam, c, p.dim);
+                    put2<VEC>(dg, mul2(m, before[r]), c, p.dim);
                     if (p.dh0 && (heads >> r) & 1)
-                        put4<VEC>(p.dh0 + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, m, c, p.dim);
+                        put2<VEC>(p.dh0 + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, m, c, p.dim);
                 }
                 dx -= p.dim, dg -= p.dim;
             }
