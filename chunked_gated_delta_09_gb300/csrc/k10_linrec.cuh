@@ -514,62 +514,76 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
 }
 
 // ---------------------------------------------------------------- backward
-// g is done with when the groups' maps are formed, x and dh are read again to finish a tile: they take one place more.
+// g is done with when the groups' maps are formed and its place then takes the tile after next; x and dh are read again to
+// finish a tile, and theirs takes the next but one when the next tile's maps are formed.
 template <typename T, typename G> struct BwdStages {
-    static constexpr int ROWS = LR_R * LR_BWD_GROUPS, GS = 2, XS = 3;
-    static constexpr uint32_t BYTES = sizeof(Tile<G, ROWS>) + 2 * sizeof(Tile<T, ROWS>);
-    Tile<G, ROWS> g[GS];
-    Tile<T, ROWS> x[XS], dh[XS];
+    static constexpr int ROWS = LR_R * LR_BWD_GROUPS;
+    Tile<G, ROWS> g[2];
+    Tile<T, ROWS> x[2], dh[2];
 };
 
 template <typename T, typename G, bool COMP, bool VEC>
-__global__ void __launch_bounds__(LR_THREADS, 2)
+__global__ void __launch_bounds__(LR_THREADS, 3)
     k10_bwd(const __grid_constant__ LinrecParams p, const __grid_constant__ LinrecMaps maps) {
     using Stages = BwdStages<T, G>;
-    constexpr int R = LR_R, ROWS = Stages::ROWS, GS = Stages::GS, S = Stages::XS;
+    constexpr int R = LR_R, ROWS = Stages::ROWS;
     extern __shared__ __align__(128) char dynamic[];
     Stages &st = *reinterpret_cast<Stages *>(dynamic);
-    __shared__ __align__(16) LinrecSmem<ROWS, S, LR_WARPS> sm;
+    __shared__ __align__(16) LinrecSmem<ROWS, 4, LR_WARPS> sm;  // full: of g's two places, of those of x and dh
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = threadIdx.x >> 4, ch = 2 * (lane & 15);
     const int rank = cluster_rank(), cb = blockIdx.x / p.cluster, c = cb * LR_CH + ch;
     const bool channels = VEC && (cb + 1) * LR_CH <= p.dim;
 
     // the scan goes from the last rows to the first, in the cluster too
     auto tile_of = [&](int k) { return (p.supers - k) * p.cluster - 1 - rank; };
-    auto fetch = [&](int k) {
-        const int tile = tile_of(k);
+    auto fetch_g = [&](int k) {
+        const int buf = k & 1, tile = tile_of(k);
         if (VEC) {
-            mbar_expect_tx(&sm.full[k % S], Stages::BYTES);
-            load_tile(&st.g[k % GS], &maps.g, cb * LR_CH, tile * ROWS, &sm.full[k % S]);
-            load_tile(&st.x[k % S], &maps.x, cb * LR_CH, tile * ROWS, &sm.full[k % S]);
-            load_tile(&st.dh[k % S], &maps.dh, cb * LR_CH, tile * ROWS, &sm.full[k % S]);
+            mbar_expect_tx(&sm.full[buf], sizeof(st.g[0]));
+            load_tile(&st.g[buf], &maps.g, cb * LR_CH, tile * ROWS, &sm.full[buf]);
         } else {
-            st.g[k % GS].bring(p.g, p.g_ts, tile, wid, cb, p);
-            st.x[k % S].bring(p.x, p.x_ts, tile, wid, cb, p);
-            st.dh[k % S].bring(p.dh, p.dh_ts, tile, wid, cb, p);
+            st.g[buf].bring(p.g, p.g_ts, tile, wid, cb, p);
             __syncwarp();
         }
     };
-    init_barriers(sm.full, S, sm.peers);
+    auto fetch_x = [&](int k) {
+        const int buf = k & 1, tile = tile_of(k);
+        if (VEC) {
+            mbar_expect_tx(&sm.full[2 + buf], 2 * sizeof(st.x[0]));
+            load_tile(&st.x[buf], &maps.x, cb * LR_CH, tile * ROWS, &sm.full[2 + buf]);
+            load_tile(&st.dh[buf], &maps.dh, cb * LR_CH, tile * ROWS, &sm.full[2 + buf]);
+        } else {
+            st.x[buf].bring(p.x, p.x_ts, tile, wid, cb, p);
+            st.dh[buf].bring(p.dh, p.dh_ts, tile, wid, cb, p);
+            __syncwarp();
+        }
+    };
+    init_barriers(sm.full, 4, sm.peers);
     check_sequences(p);
     int sa = 0, sb = 0;
     if (wid == 2) sm.ends[0].find(p, tile_of(0), sa, sb);
     cluster_sync();
-    for (int k = 0; k < 2 && k < p.supers; ++k)
-        if (!VEC || threadIdx.x == 0) fetch(k);
+    if (!VEC || threadIdx.x == 0) {
+        fetch_g(0);
+        fetch_x(0);
+        if (p.supers > 1) fetch_g(1);
+    }
     float walked = 0.f;
     for (int k = 0; k < p.supers; ++k) {
         const int buf = k & 1, tile = tile_of(k), first = group * R, row0 = tile * ROWS + first;
         const Ends<ROWS> &ends = sm.ends[buf];
-        const auto &gt = st.g[k % GS];
-        const auto &xt = st.x[k % S], &dt = st.dh[k % S];
+        const auto &gt = st.g[buf];
+        const auto &xt = st.x[buf], &dt = st.dh[buf];
         const uint32_t tcuts = ends.tail_cuts(), heads = ends.heads(group), tails = ends.tails(group);
         const bool plain = channels && (tile + 1) * ROWS <= p.rows && !__any_sync(0xffffffffu, heads | tails);
         const int warp0 = tile * ROWS + wid * LR_SAVE;  // the warp's first row
         // the h that enters it
         F2 h = plain ? *reinterpret_cast<const F2 *>(p.states + (int64_t)(warp0 / LR_SAVE) * p.dim + c)
                      : row2(warp0 < p.rows ? p.states : nullptr, warp0 / LR_SAVE, c, p.dim);
-        if (VEC) wait_phase(&sm.full[k % S], (k / S) & 1, p);
+        if (VEC) {
+            wait_phase(&sm.full[buf], (k >> 1) & 1, p);
+            wait_phase(&sm.full[2 + buf], (k >> 1) & 1, p);
+        }
         auto dh_at = [&](int r, auto any) {  // with the gradient of the last state on a sequence's last row
             F2 d = dt.get2(first + r, ch);
             if (any.value && (tails >> r) & 1) d = add2(d, row2(p.dht, ends.sequence_of(p, row0 + r), c, p.dim));
@@ -609,8 +623,11 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
         const F2 out = shfl2(heads ? B : fma2(A, h, B), lane & 15);
         if (lane >= 16) h = out;
         __syncthreads();
-        // everybody is done with this tile's g and with the tile before: their places take the tile after next
-        if (k + 2 < p.supers && (!VEC || threadIdx.x == 128)) fetch(k + 2);
+        // everybody is done with this tile's g and with x and dh of the tile before
+        if (!VEC || threadIdx.x == 128) {
+            if (k + 1 < p.supers) fetch_x(k + 1);
+            if (k + 2 < p.supers) fetch_g(k + 2);
+        }
         scan_maps<LR_WARPS, true>(sm.maps, tcuts, wid, lane, sm.total);
         totals_there(wid == 1);
         if (wid == 1) {
