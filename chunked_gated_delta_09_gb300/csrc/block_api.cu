@@ -373,7 +373,7 @@ static gdr_status clip_impl(const gdr_clip_args *a, bool scale, cudaStream_t str
     if (!a->workspace || !at(a->workspace, 16) || a->workspace_bytes < gdr_clip_workspace_bytes(a->count, total))
         return GDR_ERR_INVALID_ARG;
     double *part = (double *)a->workspace;
-    std::unique_ptr<ClipTable> t(new (std::nothrow) ClipTable);
+    std::unique_ptr<ClipTable<CLIP_TENSORS>> t(new (std::nothrow) ClipTable<CLIP_TENSORS>);
     if (!t) return GDR_ERR_OOM;
     int parts = 0;
     for (int pass = 0; pass < (scale ? 2 : 1); ++pass) {

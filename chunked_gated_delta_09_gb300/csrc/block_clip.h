@@ -10,20 +10,20 @@ constexpr int CLIP_TENSORS = 640;    // per launch; longer lists take more launc
 constexpr int CLIP_PIECE = 16384;    // elements
 constexpr int CLIP_CTAS = 152 * 4;
 
-struct ClipTable {
-    const void *grad[CLIP_TENSORS];
-    void *out[CLIP_TENSORS];
-    int64_t size[CLIP_TENSORS];
-    int64_t first[CLIP_TENSORS + 1];  // number of the tensor's first piece
+template <int N> struct ClipTable {
+    const void *grad[N];
+    void *out[N];
+    int64_t size[N];
+    int64_t first[N + 1];  // number of the tensor's first piece
     int64_t pieces;
     int count;
-    uint8_t dtype[CLIP_TENSORS], out_dtype[CLIP_TENSORS];
+    uint8_t dtype[N], out_dtype[N];
 };
-static_assert(sizeof(ClipTable) <= 32000, "the table is a kernel argument");
+static_assert(sizeof(ClipTable<CLIP_TENSORS>) <= 32000, "the table is a kernel argument");
 
-cudaError_t launch_clip_sumsq(const ClipTable &t, double *part, int parts, cudaStream_t stream);
+cudaError_t launch_clip_sumsq(const ClipTable<CLIP_TENSORS> &t, double *part, int parts, cudaStream_t stream);
 cudaError_t launch_clip_norm(const double *part, int parts, float *norm, cudaStream_t stream);
-cudaError_t launch_clip_scale(const ClipTable &t, const double *part, int parts, float *norm, float max_norm, float eps,
-                              cudaStream_t stream);
+cudaError_t launch_clip_scale(const ClipTable<CLIP_TENSORS> &t, const double *part, int parts, float *norm, float max_norm,
+                              float eps, cudaStream_t stream);
 
 }  // namespace gdr
