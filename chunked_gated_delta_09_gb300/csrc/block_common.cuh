@@ -21,12 +21,65 @@ template <typename T, int N> __device__ __forceinline__ void unpack(const Pack<T
 #pragma unroll
     for (int i = 0; i < N; ++i) o[i] = to_f32(a.v[i]);
 }
+// Two values rounded by one instruction.
+template <typename T> struct Pair;
+template <> struct Pair<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t of(float x, float y) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+};
+template <> struct Pair<__half> {
+    static __device__ __forceinline__ uint32_t of(float x, float y) {
+        const __half2 v = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+};
 template <typename T, int N> __device__ __forceinline__ void store_pack(T *p, const float (&x)[N]) {
     Pack<T, N> a;
+    if constexpr (sizeof(T) == 2 && N % 2 == 0) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(&a);
 #pragma unroll
-    for (int i = 0; i < N; ++i) a.v[i] = to_out_t<T>(x[i]);
+        for (int i = 0; i < N / 2; ++i) w[i] = Pair<T>::of(x[2 * i], x[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) a.v[i] = to_out_t<T>(x[i]);
+    }
     *reinterpret_cast<Pack<T, N> *>(p) = a;
 }
+
+// ---------------------------------------------------------------- pairs of fp32 values, one instruction for both
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+    __device__ __forceinline__ explicit F2(float x) : F2(x, x) {}
+    __device__ __forceinline__ void get(float &x, float &y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+
+// 16 bytes from global to shared memory without waiting; zeros where `on` is false.  For long contiguous rows: L2 fetches
+// 256 bytes at a time.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool on) {
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most LEFT of the thread's groups of copies are under way.
+template <int LEFT> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // n / d for n < 2^31 by one multiplication: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d) the error
 // m d - 2^(31 + s) is below d <= 2^s, so n m / 2^(31 + s) exceeds n / d by less than 1 / d.
@@ -120,6 +173,8 @@ struct StepParams {
 // CTAs that write partial column sums, at most (the workspace is sized for it).
 constexpr int NORM_MAX_PARTS = 152 * 8;
 int norm_parts(int64_t rows, int64_t dim);
+cudaError_t norm_grid(const void *kernel, int threads, int smem, int max_smem, int64_t rows, int rows_per_cta,
+                      int most, int &grid);
 
 cudaError_t launch_gated_norm_fwd(const GatedNormParams &p, cudaStream_t stream);
 cudaError_t launch_gated_norm_bwd(const GatedNormParams &p, cudaStream_t stream);

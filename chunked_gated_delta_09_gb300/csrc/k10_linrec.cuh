@@ -31,29 +31,6 @@ constexpr int LR_R = 8;                        // rows of a group
 constexpr int LR_GROUPS = 32, LR_BWD_GROUPS = 16;  // groups of a tile, 4 (backwards 2) to a warp
 static_assert(LR_SAVE == LR_BWD_GROUPS / LR_WARPS * LR_R, "a saved state enters each warp's rows of the backward");
 
-// ---------------------------------------------------------------- pairs of fp32 values, one instruction for both
-struct F2 {
-    uint64_t v;
-    __device__ __forceinline__ F2() {}
-    __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
-    __device__ __forceinline__ explicit F2(float x) : F2(x, x) {}
-    __device__ __forceinline__ void get(float &x, float &y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
-};
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return d;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-    return d;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-    return d;
-}
 // exp(g) and 1 - exp(g), both to about one unit in the last place and without a lean to one side, which a channel that
 // remembers hundreds of tokens would add up (decays near 1 that come out a quarter of a unit too low put h off by
 // 1e-5).  Cody and Waite's reduction g = n ln 2 + r, then exp(r) - 1 = r + r^2 q(r) with q a Chebyshev fit of degree 4

@@ -1,7 +1,43 @@
 // k9_norms.cu -- the norms around a block: choice by type, and the sum of the partial column sums (dweight, dscale).
+#include <mutex>
+#include <unordered_map>
+
 #include "block_common.cuh"
 
 namespace gdr {
+
+namespace {
+std::mutex g_mu;
+std::unordered_map<const void *, int> g_resident[64][33];  // per device and number of warps: CTAs that it holds
+}  // namespace
+
+// CTAs of a persistent grid: as many as the device holds at a time, no more than there are rows for, and at most `most`.
+// max_smem: with the most threads that the kernel is launched with.
+cudaError_t norm_grid(const void *kernel, int threads, int smem, int max_smem, int64_t rows, int rows_per_cta, int most, int &grid) {
+    int dev = 0, n = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        int fresh = 0;
+        int &held = dev >= 0 && dev < 64 ? g_resident[dev][threads / 32][kernel] : fresh;
+        if (!held) {
+            int sms = 0, per_sm = 0;
+            if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem)) != cudaSuccess)
+                return e;
+            if ((e = device_sm_count(&sms)) != cudaSuccess) return e;
+            if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem)) != cudaSuccess) return e;
+            if (per_sm < 1) return cudaErrorInvalidConfiguration;
+            held = sms * per_sm;
+        }
+        n = held;
+    }
+    const int64_t need = (rows + rows_per_cta - 1) / rows_per_cta;
+    if (n > need) n = (int)need;
+    if (n > most) n = most;
+    grid = n < 1 ? 1 : n;
+    return cudaSuccess;
+}
 
 // Rows of partial sums that a backward may write: as many CTAs as its grid can have.
 int norm_parts(int64_t rows, int64_t dim) {
@@ -9,25 +45,31 @@ int norm_parts(int64_t rows, int64_t dim) {
     return (int)(rows < most ? (rows < 1 ? 1 : rows) : most);
 }
 
-// out[col] = sum over the partial rows, in a fixed order: a CTA takes 32 columns, its 32 warps take every 32nd row
-// each, and the warps' sums are added in order.
-__global__ void __launch_bounds__(1024) k9_colsum(const float *part, int parts, int dim, void *out, int dtype) {
+// out[col] = sum over the partial rows, in a fixed order: a CTA takes 32 columns of one of the sums, its 32 warps take every
+// 32nd row each, and the warps' sums are added in order.
+__global__ void __launch_bounds__(1024) k9_colsum(const float *part, int parts, int dim, void *out0, int dtype0, void *out1,
+                                                  int dtype1) {
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    part += (size_t)blockIdx.y * parts * dim;
     float a = 0.f;
-    if (col < dim)
+    if (col < dim) {
+#pragma unroll 8
         for (int r = wid; r < parts; r += 32) a += part[(size_t)r * dim + col];
+    }
     s[wid][lane] = a;
     __syncthreads();
     if (wid == 0 && col < dim) {
         float t = 0.f;
+#pragma unroll
         for (int i = 0; i < 32; ++i) t += s[i][lane];
-        store_scalar(out, col, t, dtype);
+        store_scalar(blockIdx.y ? out1 : out0, col, t, blockIdx.y ? dtype1 : dtype0);
     }
 }
 
-cudaError_t launch_colsum(const float *part, int parts, int dim, void *out, int dtype, cudaStream_t stream) {
-    k9_colsum<<<(dim + 31) / 32, 1024, 0, stream>>>(part, parts, dim, out, dtype);
+cudaError_t launch_colsum(const float *part, int parts, int dim, int sums, void *out0, int dtype0, void *out1, int dtype1,
+                          cudaStream_t stream) {
+    k9_colsum<<<dim3((dim + 31) / 32, sums), 1024, 0, stream>>>(part, parts, dim, out0, dtype0, out1, dtype1);
     return cudaGetLastError();
 }
 

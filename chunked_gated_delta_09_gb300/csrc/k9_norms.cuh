@@ -6,11 +6,11 @@
 //     t = dy w ;  dr = rs t - r rs^3 mean(t r) + dres ;  dx = s dr ;  dw = sum of dy r rs ;  ds = sum of dr x
 //
 // Both row sums of a backward (of squares and of t x) come from one pass over values that stay in registers, so
-// every input is read once and every output written once: the kernels are bound by HBM.  A row belongs to a group
-// of G threads, each holding NV pieces of VEC elements; groups of up to 32 threads sum by shuffles, larger ones
-// (one row per CTA) through shared memory.  The grid is persistent, so the weights are read once per thread and the
-// column sums of a backward (dw, ds) stay in registers until the CTA writes its partial row; k9_colsum adds the
-// partial rows in a fixed order.
+// every input is read once and every output written once: the kernels are bound by HBM.  A row belongs to 8, 16 or 32
+// lanes or to a whole CTA, a thread holding one piece of VEC elements where the row fits 1024 threads.  Lanes sum by
+// shuffles, CTAs through shared memory.  The grid is persistent: the weights are read once per thread, and the column sums
+// of a backward (dw, ds) stay in registers until the CTA writes its partial row, which k9_colsum adds in a fixed order.
+// The rows ahead come in one of three ways (see Ahead), whichever measured fastest for the kernel.
 #pragma once
 
 #include "block_common.cuh"
@@ -21,33 +21,40 @@ namespace {
 constexpr int NORM_THREADS = 256;  // of a CTA whose groups are warps or parts of one
 
 template <typename T> __device__ __forceinline__ float sigmoid_t(float z) {
-    // 16-bit results: the fast exponential and reciprocal are 3e-7 off, far below the result's 4e-3 or 5e-4
-    if constexpr (sizeof(T) == 2) return __fdividef(1.f, 1.f + __expf(-z));
+    if constexpr (sizeof(T) == 2) {
+        // 16-bit results: the approximate exponential and reciprocal are 3e-7 off, far below the result's 4e-3 or 5e-4
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(1.f + e));
+        return e;
+    }
     return 1.f / (1.f + expf(-z));
 }
+constexpr int ACT_NONE = 2;  // besides the C interface's silu and sigmoid
 
-// Sums of two values over the group's G threads, in the same order whatever the row.
+// Sums of two values over the row's threads (G lanes, or the whole CTA for G = 0), in the same order whatever the row.
 template <int G> struct GroupSum {
-    static constexpr int NW = G > 32 ? G / 32 : 1;
-    float2 *red;  // [2][NW] in shared memory (G > 32)
-    int buf;
-    __device__ __forceinline__ explicit GroupSum(float2 *r) : red(r), buf(0) {}
-    __device__ __forceinline__ float2 operator()(float a, float b) {
+    float2 *red;  // [2][warps] in shared memory (G = 0)
+    int buf = 0;
+    __device__ __forceinline__ explicit GroupSum(float2 *r) : red(r) {}
+    // TWO: b is wanted too
+    template <bool TWO = true> __device__ __forceinline__ float2 operator()(float a, float b) {
 #pragma unroll
-        for (int o = (G < 32 ? G : 32) / 2; o > 0; o >>= 1) {
+        for (int o = (G ? G : 32) / 2; o > 0; o >>= 1) {
             a += __shfl_xor_sync(0xffffffffu, a, o);
-            b += __shfl_xor_sync(0xffffffffu, b, o);
+            if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
         }
-        if constexpr (G > 32) {
+        if constexpr (G == 0) {
             // two buffers in turn: a warp can only be back at this one after the next row's barrier
-            if ((threadIdx.x & 31) == 0) red[buf * NW + (threadIdx.x >> 5)] = make_float2(a, b);
+            const int nw = blockDim.x / 32, lane = threadIdx.x & 31;
+            if (lane == 0) red[buf * 32 + (threadIdx.x >> 5)] = make_float2(a, b);
             __syncthreads();
-            a = b = 0.f;
+            const float2 x = lane < nw ? red[buf * 32 + lane] : make_float2(0.f, 0.f);
+            a = x.x, b = x.y;
 #pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                const float2 x = red[buf * NW + i];
-                a += x.x;
-                b += x.y;
+            for (int o = 16; o > 0; o >>= 1) {
+                a += __shfl_xor_sync(0xffffffffu, a, o);
+                if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
             }
             buf ^= 1;
         }
@@ -64,45 +71,138 @@ struct NormGrad {
     __device__ __forceinline__ float operator()(float tv, float xv) const { return fmaf(tv, t, -xv * x); }
 };
 
-// The thread's columns: piece i starts at column (t + i G) VEC.
+// The thread's columns: piece i starts at column (t + i threads) VEC; threads: of a row.
 template <int VEC, int G, int NV> struct Cols {
-    int t;
+    int t, step, dim;
     bool on[NV];
-    __device__ __forceinline__ Cols(int t_, int dim) : t(t_) {
+    __device__ __forceinline__ explicit Cols(int dim_) : t(G ? threadIdx.x % (G ? G : 1) : threadIdx.x), step(G ? G : blockDim.x), dim(dim_) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) on[i] = (t + i * G) * VEC < dim;
+        for (int i = 0; i < NV; ++i) on[i] = (t + i * step) * VEC < dim;
     }
-    __device__ __forceinline__ int at(int i) const { return (t + i * G) * VEC; }
+    __device__ __forceinline__ int at(int i) const { return (t + i * step) * VEC; }
 };
+// Rows that a CTA works on at a time, and the thread's among them.
+template <int G> __device__ __forceinline__ int cta_rows() { return G ? NORM_THREADS / (G ? G : 1) : 1; }
+template <int G> __device__ __forceinline__ int cta_row() { return G ? threadIdx.x / (G ? G : 1) : 0; }
 
-template <int VEC, int G, int NV>
-__device__ __forceinline__ void load_cols(const void *p, int dt, const Cols<VEC, G, NV> &c, float fill,
-                                          float (&o)[NV][VEC]) {
+// How the rows ahead come.
+//   RING   by asynchronous copies to places in shared memory, several rows ahead, which takes no registers: the backward
+//          kernels (32768 x 16 x 128 bf16 after a block 0.125 ms; PAIR 0.136; 48763 x 4096 bf16 before one 0.309; PAIR 0.425),
+//          and the forward before a block on a 16-bit stream (48763 x 4096 0.253 ms; PAIR 0.271)
+//   PAIR   the next row's pieces in registers while a row is worked on: the forward after a block (32768 x 16 x 128 bf16
+//          0.066 ms; RING 0.070), and before one on an fp32 stream (32768 x 2048 0.127; RING 0.140)
+//   NONE   a row's pieces when it is its turn, other CTAs covering the wait: single elements and rows of several pieces to a
+//          thread, which leave no registers (20000 x 1001 fp32 stream, backward 0.117 ms; PAIR 0.144)
+enum class Ahead { NONE, PAIR, RING };
+
+// How a thread gets its pieces of a row of one tensor; zeros where there is nothing.  In a RING a piece of two 16-byte places
+// (fp32 beside 16-bit types) is copied by the lanes of the row's part in the order of memory, so that each instruction
+// covers whole sectors.
+template <typename T, int VEC, int G, int NV, Ahead A> struct Feed {
+    static constexpr int N = A == Ahead::RING ? VEC * (int)sizeof(T) / 16 : 0;  // 16-byte places of a thread
+    static constexpr int L = G ? G : 32;                                        // lanes that copy for each other
+    Pack<T, VEC> v[A == Ahead::RING ? 1 : NV];
+    static __device__ __forceinline__ int place_of(int chunk) {  // (lanes that read two each hit different banks)
+        return 16 * (N == 2 ? chunk ^ ((chunk >> 3) & 1) : chunk);
+    }
+    __device__ __forceinline__ void issue(char *place, const void *p, int64_t at, const Cols<VEC, G, NV> &c, bool live) {
+        if constexpr (A == Ahead::RING) {
+            const int lane = threadIdx.x % L, first = threadIdx.x - lane, t0 = c.t - lane;  // of the lanes
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+            for (int k = 0; k < N; ++k) {
+                const int chunk = lane + k * L, col = t0 * VEC + chunk * (16 / (int)sizeof(T));
+                const bool on = live && col < c.dim;
+                copy16(place + place_of(first * N + chunk), reinterpret_cast<const T *>(p) + (on ? at + col : 0), on);
+            }
+        } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[i][j] = p && c.on[i] ? load_scalar(p, c.at(i) + j, dt) : fill;
+            for (int i = 0; i < NV; ++i) {
+                v[i] = {};
+                if (live && c.on[i]) v[i] = load_pack<T, VEC>(reinterpret_cast<const T *>(p) + at + c.at(i));
+            }
+        }
+    }
+    __device__ __forceinline__ void get(const char *place, int i, float (&o)[VEC]) const {
+        if constexpr (A == Ahead::RING) {
+            Pack<T, VEC> a;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                reinterpret_cast<uint4 *>(&a)[k] = *reinterpret_cast<const uint4 *>(place + place_of(threadIdx.x * N + k));
+            unpack<T, VEC>(a, o);
+        } else {
+            unpack<T, VEC>(v[i], o);
+        }
+    }
+};
+template <int VEC, int NV> constexpr Ahead ahead_or_none(Ahead a) { return VEC == 1 || NV > 1 ? Ahead::NONE : a; }
+
+// Rows ahead for `places` 16-byte places of a thread and row, of `budget` places (12: 1024 threads of an SM can have them).
+constexpr int norm_ahead(int places, int budget = 12) {
+    return places == 0 ? 1 : budget / places < 2 ? 2 : budget / places > 6 ? 6 : budget / places;
 }
 
-// The CTA's column sums to its partial row: the groups of a CTA are added in order.
+// The weights of a thread's columns, in registers unless it has several pieces, and its column sums, which then lie in
+// places of its own in shared memory.
+template <int VEC, int G, int NV> struct Weights {
+    static constexpr bool KEPT = NV * VEC <= 8 || VEC == 1;
+    const void *p;
+    int dt;
+    float fill, v[KEPT ? NV : 1][KEPT ? VEC : 1];
+    __device__ __forceinline__ Weights(const void *p_, int dt_, const Cols<VEC, G, NV> &c, float fill_) : p(p_), dt(dt_), fill(fill_) {
+        if constexpr (KEPT)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) v[i][j] = p && c.on[i] ? load_scalar(p, c.at(i) + j, dt) : fill;
+    }
+    __device__ __forceinline__ void get(const Cols<VEC, G, NV> &c, int i, float (&o)[VEC]) const {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            if constexpr (KEPT) o[j] = v[i][j];
+            else o[j] = p && c.on[i] ? load_scalar(p, c.at(i) + j, dt) : fill;
+        }
+    }
+};
+template <int VEC, int G, int NV> struct Sums {
+    static constexpr bool KEPT = NV * VEC <= 8 || VEC == 1;
+    static constexpr int SHARED = KEPT ? 0 : NV * VEC;  // floats of a thread
+    float v[KEPT ? NV : 1][KEPT ? VEC : 1];
+    float *s;
+    __device__ __forceinline__ explicit Sums(float *shared) : s(shared) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) at(i, j) = 0.f;
+    }
+    __device__ __forceinline__ float &at(int i, int j) {
+        if constexpr (KEPT) return v[i][j];
+        return s[(i * VEC + j) * blockDim.x + threadIdx.x];
+    }
+};
+
+template <typename T, int VEC, int G, int NV>
+__device__ __forceinline__ void store_piece(void *p, int64_t at, const Cols<VEC, G, NV> &c, int i, bool live,
+                                            const float (&x)[VEC]) {
+    if (live && c.on[i]) store_pack<T, VEC>(reinterpret_cast<T *>(p) + at + c.at(i), x);
+}
+
+// The CTA's column sums to its partial row: the rows' threads are added in order, in `smem` that nothing else uses by then.
 template <int VEC, int G, int NV>
-__device__ __forceinline__ void write_part(float *part, float *smem, const Cols<VEC, G, NV> &c, int dim,
-                                           const float (&acc)[NV][VEC]) {
-    constexpr int RPC = G > 32 ? 1 : NORM_THREADS / G;
-    if constexpr (RPC == 1) {
+__device__ __forceinline__ void write_part(float *part, float *smem, const Cols<VEC, G, NV> &c, int dim, Sums<VEC, G, NV> &acc) {
+    if constexpr (G == 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (c.on[i])
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) part[c.at(i) + j] = acc[i][j];
+                for (int j = 0; j < VEC; ++j) part[c.at(i) + j] = acc.at(i, j);
     } else {
-        constexpr int W = G * NV * VEC;  // columns held by a group
+        constexpr int W = G * NV * VEC, RPC = NORM_THREADS / G;  // columns held by a row's threads
         const int gi = threadIdx.x / G;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) smem[gi * W + c.at(i) + j] = acc[i][j];
+            for (int j = 0; j < VEC; ++j) smem[gi * W + c.at(i) + j] = acc.at(i, j);
         __syncthreads();
         for (int col = threadIdx.x; col < dim; col += NORM_THREADS) {
             float s = 0.f;
@@ -112,328 +212,418 @@ __device__ __forceinline__ void write_part(float *part, float *smem, const Cols<
     }
 }
 
-template <int VEC, int G, int NV> constexpr int norm_threads() { return G > 32 ? G : NORM_THREADS; }
-template <int VEC, int G, int NV> constexpr int part_smem() {
-    return G > 32 ? 1 : NORM_THREADS / G * G * NV * VEC;  // floats
+// The rows of a persistent CTA.  In: a row's feeds; issue(in, place, row, live), work(in, place, row, live).
+template <class In, Ahead A, int G, int S, int PLACES, class Issue, class Work>
+__device__ __forceinline__ void walk_rows(uint32_t rows, char *ring, Issue issue, Work work) {
+    const uint32_t step = gridDim.x * cta_rows<G>();
+    // (whole warps stay together: a row's lanes may lie beyond the last row)
+    uint32_t base = blockIdx.x * cta_rows<G>(), row = base + cta_row<G>();
+    if constexpr (A == Ahead::RING) {
+        In in;
+        const uint32_t bytes = PLACES * 16 * blockDim.x;
+#pragma unroll
+        for (int k = 0; k < S - 1; ++k) {
+            issue(in, ring + k * bytes, row + k * step, row + k * step < rows);
+            copies_issued();
+        }
+        uint32_t slot = 0, ahead = S - 1;
+        for (; base < rows; base += step, row += step) {
+            __syncwarp();  // every lane has read the row before, whose place is filled now
+            issue(in, ring + ahead * bytes, row + (S - 1) * step, row + (S - 1) * step < rows);
+            copies_issued();
+            copies_wait<S - 1>();
+            __syncwarp();
+            work(in, ring + slot * bytes, row, row < rows);
+            slot = slot + 1 == S ? 0 : slot + 1;
+            ahead = ahead + 1 == S ? 0 : ahead + 1;
+        }
+        copies_wait<0>();
+    } else if constexpr (A == Ahead::PAIR) {
+        In a, b;  // (two copies of the work, so that no register waits to be moved)
+        issue(a, ring, row, row < rows);
+        for (; base < rows; base += step, row += step) {
+            issue(b, ring, row + step, row + step < rows);
+            work(a, ring, row, row < rows);
+            if ((base += step) >= rows) break;
+            row += step;
+            issue(a, ring, row + step, row + step < rows);
+            work(b, ring, row, row < rows);
+        }
+    } else {
+        for (; base < rows; base += step, row += step) {
+            In in;
+            issue(in, ring, row, row < rows);
+            work(in, ring, row, row < rows);
+        }
+    }
 }
+
+// What a kernel has of shared memory: the rows ahead (PLACES 16-byte places for each thread and row), in which the column
+// sums are added at the end, or the sums themselves.
+template <typename T, int VEC, int G, int NV> struct GateFwd {
+    static constexpr Ahead A = ahead_or_none<VEC, NV>(Ahead::PAIR);
+    static constexpr int PLACES = 2 * Feed<T, VEC, G, NV, A>::N, S = norm_ahead(PLACES);
+    static constexpr int bytes(int threads) { return S * PLACES * 16 * threads; }
+};
+template <int VEC, int G, int NV> constexpr int sums_bytes(int sums, int threads) {
+    return sums * Sums<VEC, G, NV>::SHARED * 4 * threads + (G ? 4 * threads * NV * VEC : 0);
+}
+template <typename T, int VEC, int G, int NV> struct GateBwd {
+    static constexpr Ahead A = ahead_or_none<VEC, NV>(Ahead::RING);
+    static constexpr int PLACES = 3 * Feed<T, VEC, G, NV, A>::N, S = norm_ahead(PLACES);
+    static constexpr int bytes(int threads) {
+        const int a = S * PLACES * 16 * threads, b = sums_bytes<VEC, G, NV>(1, threads);
+        return a > b ? a : b;
+    }
+};
 
 // ---------------------------------------------------------------- after a block
-template <typename T, int VEC, int G, int NV>
-__global__ void __launch_bounds__(norm_threads<VEC, G, NV>()) k9_gated_fwd(const GatedNormParams p) {
-    constexpr int RPC = G > 32 ? 1 : NORM_THREADS / G;
-    __shared__ float2 red[2 * GroupSum<G>::NW];
+template <int ACT, typename T, int VEC, int G, int NV, class L>
+__device__ __forceinline__ void gated_fwd(const GatedNormParams &p, char *ring) {
+    struct In {
+        Feed<T, VEC, G, NV, L::A> x, z;
+    };
+    __shared__ float2 red[G ? 1 : 64];
     GroupSum<G> sum(red);
-    const Cols<VEC, G, NV> c(threadIdx.x % G, p.dim);
-    float w[NV][VEC];
-    load_cols<VEC, G, NV>(p.weight, p.weight_dtype, c, 1.f, w);
+    const Cols<VEC, G, NV> c(p.dim);
+    const Weights<VEC, G, NV> weight(p.weight, p.weight_dtype, c, 1.f);
     const float inv_dim = 1.f / (float)p.dim;
-    for (int64_t base = (int64_t)blockIdx.x * RPC; base < p.rows; base += (int64_t)gridDim.x * RPC) {
-        const uint32_t row = (uint32_t)base + threadIdx.x / G;
-        const bool live = row < p.rows;
-        const T *x = reinterpret_cast<const T *>(p.x) + (live ? p.xm.at(row, p.heads) : 0);
-        const T *z = reinterpret_cast<const T *>(p.z) + (live ? p.zm.at(row, p.heads) : 0);
-        float xv[NV][VEC], zv[NV][VEC], s1 = 0.f;
+    const int zo = L::PLACES / 2 * 16 * blockDim.x;
+    walk_rows<In, L::A, G, L::S, L::PLACES>(
+        p.rows, ring,
+        [&](In &in, char *at, uint32_t row, bool live) {
+            in.x.issue(at, p.x, live ? p.xm.at(row, p.heads) : 0, c, live);
+            if (ACT != ACT_NONE) in.z.issue(at + zo, p.z, live ? p.zm.at(row, p.heads) : 0, c, live);
+        },
+        [&](const In &in, const char *at, uint32_t row, bool live) {
+            float x[NV][VEC], s1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            Pack<T, VEC> a = {}, b = {};
-            if (live && c.on[i]) {
-                a = load_pack<T, VEC>(x + c.at(i));
-                if (p.z) b = load_pack<T, VEC>(z + c.at(i));
+            for (int i = 0; i < NV; ++i) {
+                in.x.get(at, i, x[i]);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s1 = fmaf(x[i][j], x[i][j], s1);
             }
-            unpack<T, VEC>(a, xv[i]);
-            unpack<T, VEC>(b, zv[i]);
-        }
+            const float rs = rsqrtf(sum.template operator()<false>(s1, 0.f).x * inv_dim + p.eps);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                float y[VEC], z[VEC], w[VEC];
+                weight.get(c, i, w);
+                if (ACT != ACT_NONE) in.z.get(at + zo, i, z);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) s1 = fmaf(xv[i][j], xv[i][j], s1);
-        const float rs = rsqrtf(sum(s1, 0.f).x * inv_dim + p.eps);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float y[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float a = 1.f;
-                if (p.z) {
-                    a = sigmoid_t<T>(zv[i][j]);
-                    if (p.act == 0) a *= zv[i][j];
+                for (int j = 0; j < VEC; ++j) {
+                    y[j] = x[i][j] * rs * w[j];
+                    if (ACT != ACT_NONE) y[j] *= ACT == 0 ? z[j] * sigmoid_t<T>(z[j]) : sigmoid_t<T>(z[j]);
                 }
-                y[j] = xv[i][j] * rs * w[i][j] * a;
+                store_piece<T>(p.y, (int64_t)row * p.dim, c, i, live, y);
             }
-            if (live && c.on[i])
-                store_pack<T, VEC>(reinterpret_cast<T *>(p.y) + (size_t)row * p.dim + c.at(i), y);
-        }
-    }
+        });
 }
 
-template <typename T, int VEC, int G, int NV>
-__global__ void __launch_bounds__(norm_threads<VEC, G, NV>()) k9_gated_bwd(const GatedNormParams p) {
-    constexpr int RPC = G > 32 ? 1 : NORM_THREADS / G;
-    __shared__ float2 red[2 * GroupSum<G>::NW];
-    __shared__ float psm[part_smem<VEC, G, NV>()];
+template <int ACT, typename T, int VEC, int G, int NV, class L>
+__device__ __forceinline__ void gated_bwd(const GatedNormParams &p, char *ring, float *shared) {
+    struct In {
+        Feed<T, VEC, G, NV, L::A> x, dy, z;
+    };
+    __shared__ float2 red[G ? 1 : 64];
     GroupSum<G> sum(red);
-    const Cols<VEC, G, NV> c(threadIdx.x % G, p.dim);
-    float w[NV][VEC], dw[NV][VEC] = {};
-    load_cols<VEC, G, NV>(p.weight, p.weight_dtype, c, 1.f, w);
+    const Cols<VEC, G, NV> c(p.dim);
+    const Weights<VEC, G, NV> weight(p.weight, p.weight_dtype, c, 1.f);
+    Sums<VEC, G, NV> dw(shared);
     const float inv_dim = 1.f / (float)p.dim;
-    for (int64_t base = (int64_t)blockIdx.x * RPC; base < p.rows; base += (int64_t)gridDim.x * RPC) {
-        const uint32_t row = (uint32_t)base + threadIdx.x / G;
-        const bool live = row < p.rows;
-        const T *x = reinterpret_cast<const T *>(p.x) + (live ? p.xm.at(row, p.heads) : 0);
-        const T *z = reinterpret_cast<const T *>(p.z) + (live ? p.zm.at(row, p.heads) : 0);
-        const T *dy = reinterpret_cast<const T *>(p.dy) + (live ? p.dym.at(row, p.heads) : 0);
-        float xv[NV][VEC], up[NV][VEC], dzv[NV][VEC], s1 = 0.f, s2 = 0.f;  // up = dy act(z), dzv = dy act'(z)
+    const int one = L::PLACES / 3 * 16 * blockDim.x;
+    walk_rows<In, L::A, G, L::S, L::PLACES>(
+        p.rows, ring,
+        [&](In &in, char *at, uint32_t row, bool live) {
+            in.x.issue(at, p.x, live ? p.xm.at(row, p.heads) : 0, c, live);
+            in.dy.issue(at + one, p.dy, live ? p.dym.at(row, p.heads) : 0, c, live);
+            if (ACT != ACT_NONE) in.z.issue(at + 2 * one, p.z, live ? p.zm.at(row, p.heads) : 0, c, live);
+        },
+        [&](const In &in, const char *at, uint32_t row, bool live) {
+            float x[NV][VEC], up[NV][VEC], dz[NV][VEC], s1 = 0.f, s2 = 0.f;  // up = dy act(z), dz = dy act'(z)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            Pack<T, VEC> a = {}, b = {}, d = {};
-            if (live && c.on[i]) {
-                a = load_pack<T, VEC>(x + c.at(i));
-                d = load_pack<T, VEC>(dy + c.at(i));
-                if (p.z) b = load_pack<T, VEC>(z + c.at(i));
-            }
-            unpack<T, VEC>(a, xv[i]);
-            unpack<T, VEC>(d, up[i]);
-            unpack<T, VEC>(b, dzv[i]);
-        }
+            for (int i = 0; i < NV; ++i) {
+                float w[VEC];
+                weight.get(c, i, w);
+                in.x.get(at, i, x[i]);
+                in.dy.get(at + one, i, up[i]);
+                if (ACT != ACT_NONE) in.z.get(at + 2 * one, i, dz[i]);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                if (p.z) {
-                    const float z1 = dzv[i][j], d = up[i][j], sg = sigmoid_t<T>(z1), rest = sg * (1.f - sg);
-                    up[i][j] = d * (p.act == 0 ? z1 * sg : sg);
-                    dzv[i][j] = d * (p.act == 0 ? fmaf(z1, rest, sg) : rest);
+                for (int j = 0; j < VEC; ++j) {
+                    if (ACT != ACT_NONE) {
+                        const float z = dz[i][j], d = up[i][j], sg = sigmoid_t<T>(z), rest = fmaf(-sg, sg, sg);
+                        up[i][j] = d * (ACT == 0 ? z * sg : sg);
+                        dz[i][j] = d * (ACT == 0 ? fmaf(z, rest, sg) : rest);
+                    }
+                    s1 = fmaf(x[i][j], x[i][j], s1);
+                    s2 = fmaf(up[i][j] * w[j], x[i][j], s2);
                 }
-                s1 = fmaf(xv[i][j], xv[i][j], s1);
-                s2 = fmaf(up[i][j] * w[i][j], xv[i][j], s2);
             }
-        const float2 s = sum(s1, s2);
-        const float rs = rsqrtf(s.x * inv_dim + p.eps);
-        const NormGrad q(rs, s.y * inv_dim, p.dim, p.eps);
+            const float2 s = sum(s1, s2);
+            const float rs = rsqrtf(s.x * inv_dim + p.eps);
+            const NormGrad q(rs, s.y * inv_dim, p.dim, p.eps);
+            const int64_t o = (int64_t)row * p.dim;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float dx[VEC], dz[VEC];
+            for (int i = 0; i < NV; ++i) {
+                float dx[VEC], w[VEC];
+                weight.get(c, i, w);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float xr = xv[i][j] * rs;
-                dx[j] = q(up[i][j] * w[i][j], xv[i][j]);
-                dz[j] = dzv[i][j] * xr * w[i][j];
-                dw[i][j] = fmaf(up[i][j], xr, dw[i][j]);  // (rows past the end hold zeros)
+                for (int j = 0; j < VEC; ++j) {
+                    const float xr = x[i][j] * rs;
+                    dx[j] = q(up[i][j] * w[j], x[i][j]);
+                    if (ACT != ACT_NONE) dz[i][j] *= xr * w[j];
+                    dw.at(i, j) = fmaf(up[i][j], xr, dw.at(i, j));  // (rows past the end hold zeros)
+                }
+                store_piece<T>(p.dx, o, c, i, live, dx);
+                if (ACT != ACT_NONE) store_piece<T>(p.dz, o, c, i, live, dz[i]);
             }
-            if (live && c.on[i]) {
-                const size_t o = (size_t)row * p.dim + c.at(i);
-                store_pack<T, VEC>(reinterpret_cast<T *>(p.dx) + o, dx);
-                if (p.z) store_pack<T, VEC>(reinterpret_cast<T *>(p.dz) + o, dz);
-            }
-        }
-    }
-    if (p.dweight) write_part<VEC, G, NV>(p.part + (size_t)blockIdx.x * p.dim, psm, c, p.dim, dw);
+        });
+    if (p.dweight) write_part<VEC, G, NV>(p.part + (size_t)blockIdx.x * p.dim, shared, c, p.dim, dw);
+}
+
+template <typename T, int VEC, int G, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k9_gated_fwd(const __grid_constant__ GatedNormParams p) {
+    extern __shared__ __align__(16) char norm_smem[];
+    using L = GateFwd<T, VEC, G, NV>;
+    if (!p.z) gated_fwd<ACT_NONE, T, VEC, G, NV, L>(p, norm_smem);
+    else if (p.act == 0) gated_fwd<0, T, VEC, G, NV, L>(p, norm_smem);
+    else gated_fwd<1, T, VEC, G, NV, L>(p, norm_smem);
+}
+template <typename T, int VEC, int G, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k9_gated_bwd(const __grid_constant__ GatedNormParams p) {
+    extern __shared__ __align__(16) char norm_smem[];
+    using L = GateBwd<T, VEC, G, NV>;
+    float *shared = reinterpret_cast<float *>(norm_smem);
+    if (!p.z) gated_bwd<ACT_NONE, T, VEC, G, NV, L>(p, norm_smem, shared);
+    else if (p.act == 0) gated_bwd<0, T, VEC, G, NV, L>(p, norm_smem, shared);
+    else gated_bwd<1, T, VEC, G, NV, L>(p, norm_smem, shared);
 }
 
 // ---------------------------------------------------------------- before a block
-template <typename T, typename R, int VEC, int G, int NV>
-__global__ void __launch_bounds__(norm_threads<VEC, G, NV>()) k9_add_fwd(const AddNormParams p) {
-    constexpr int RPC = G > 32 ? 1 : NORM_THREADS / G;
-    __shared__ float2 red[2 * GroupSum<G>::NW];
-    GroupSum<G> sum(red);
-    const Cols<VEC, G, NV> c(threadIdx.x % G, p.dim);
-    float w[NV][VEC], sc[NV][VEC];
-    load_cols<VEC, G, NV>(p.weight, p.weight_dtype, c, 1.f, w);
-    load_cols<VEC, G, NV>(p.scale_vec, p.scale_dtype, c, p.scale, sc);
-    const float inv_dim = 1.f / (float)p.dim;
-    for (int64_t base = (int64_t)blockIdx.x * RPC; base < p.rows; base += (int64_t)gridDim.x * RPC) {
-        const uint32_t row = (uint32_t)base + threadIdx.x / G;
-        const bool live = row < p.rows;
-        const T *x = reinterpret_cast<const T *>(p.x) + (int64_t)row * p.x_ts;
-        const R *res = reinterpret_cast<const R *>(p.residual) + (int64_t)row * p.r_ts;
-        float rv[NV][VEC], s1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            Pack<T, VEC> a = {};
-            Pack<R, VEC> b = {};
-            if (live && c.on[i]) {
-                a = load_pack<T, VEC>(x + c.at(i));
-                if (p.residual) b = load_pack<R, VEC>(res + c.at(i));
-            }
-            float xv[VEC];
-            unpack<T, VEC>(a, xv);
-            unpack<R, VEC>(b, rv[i]);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) rv[i][j] = fmaf(sc[i][j], xv[j], rv[i][j]);
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) s1 = fmaf(rv[i][j], rv[i][j], s1);
-        const float rs = rsqrtf(sum(s1, 0.f).x * inv_dim + p.eps);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (live && c.on[i]) {
-                float y[VEC];
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) y[j] = rv[i][j] * rs * w[i][j];
-                store_pack<T, VEC>(reinterpret_cast<T *>(p.y) + (size_t)row * p.dim + c.at(i), y);
-                if (p.residual_out)
-                    store_pack<R, VEC>(reinterpret_cast<R *>(p.residual_out) + (int64_t)row * p.ro_ts + c.at(i), rv[i]);
-            }
+template <typename T, typename R, int VEC, int G, int NV> struct AddFwd {
+    static constexpr Ahead A = ahead_or_none<VEC, NV>(sizeof(R) == 4 ? Ahead::PAIR : Ahead::RING);
+    static constexpr int PLACES = 1 * Feed<T, VEC, G, NV, A>::N + 1 * Feed<R, VEC, G, NV, A>::N, S = norm_ahead(PLACES, 6);
+    static constexpr int bytes(int threads) { return S * PLACES * 16 * threads; }
+};
+template <typename T, typename R, int VEC, int G, int NV> struct AddBwd {
+    static constexpr Ahead A = ahead_or_none<VEC, NV>(Ahead::RING);
+    static constexpr int PLACES = 2 * Feed<T, VEC, G, NV, A>::N + 2 * Feed<R, VEC, G, NV, A>::N, S = norm_ahead(PLACES);
+    static constexpr int bytes(int threads) {
+        const int a = S * PLACES * 16 * threads, b = sums_bytes<VEC, G, NV>(2, threads);
+        return a > b ? a : b;
     }
+};
+
+template <typename T, typename R, int VEC, int G, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k9_add_fwd(const __grid_constant__ AddNormParams p) {
+    using L = AddFwd<T, R, VEC, G, NV>;
+    using X = Feed<T, VEC, G, NV, L::A>;
+    struct In {
+        X x;
+        Feed<R, VEC, G, NV, L::A> r;
+    };
+    extern __shared__ __align__(16) char norm_smem[];
+    __shared__ float2 red[G ? 1 : 64];
+    GroupSum<G> sum(red);
+    const Cols<VEC, G, NV> c(p.dim);
+    const Weights<VEC, G, NV> weight(p.weight, p.weight_dtype, c, 1.f), scale(p.scale_vec, p.scale_dtype, c, p.scale);
+    const float inv_dim = 1.f / (float)p.dim;
+    const int ro = X::N * 16 * blockDim.x;
+    walk_rows<In, L::A, G, L::S, L::PLACES>(
+        p.rows, norm_smem,
+        [&](In &in, char *at, uint32_t row, bool live) {
+            in.x.issue(at, p.x, (int64_t)row * p.x_ts, c, live);
+            in.r.issue(at + ro, p.residual, (int64_t)row * p.r_ts, c, live && p.residual);
+        },
+        [&](const In &in, const char *at, uint32_t row, bool live) {
+            float r[NV][VEC], s1 = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float x[VEC], sc[VEC];
+                scale.get(c, i, sc);
+                in.x.get(at, i, x);
+                in.r.get(at + ro, i, r[i]);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    r[i][j] = fmaf(sc[j], x[j], r[i][j]);
+                    s1 = fmaf(r[i][j], r[i][j], s1);
+                }
+            }
+            if (p.residual_out)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) store_piece<R>(p.residual_out, (int64_t)row * p.ro_ts, c, i, live, r[i]);
+            const float rs = rsqrtf(sum.template operator()<false>(s1, 0.f).x * inv_dim + p.eps);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float y[VEC], w[VEC];
+                weight.get(c, i, w);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[j] = r[i][j] * rs * w[j];
+                store_piece<T>(p.y, (int64_t)row * p.dim, c, i, live, y);
+            }
+        });
 }
 
-template <typename T, typename R, int VEC, int G, int NV>
-__global__ void __launch_bounds__(norm_threads<VEC, G, NV>()) k9_add_bwd(const AddNormParams p) {
-    constexpr int RPC = G > 32 ? 1 : NORM_THREADS / G;
-    __shared__ float2 red[2 * GroupSum<G>::NW];
-    __shared__ float psm[part_smem<VEC, G, NV>()];
+template <typename T, typename R, int VEC, int G, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k9_add_bwd(const __grid_constant__ AddNormParams p) {
+    using L = AddBwd<T, R, VEC, G, NV>;
+    using X = Feed<T, VEC, G, NV, L::A>;
+    using Res = Feed<R, VEC, G, NV, L::A>;
+    struct In {
+        X dy, x;
+        Res r, dres;
+    };
+    extern __shared__ __align__(16) char norm_smem[];
+    float *shared = reinterpret_cast<float *>(norm_smem);
+    __shared__ float2 red[G ? 1 : 64];
     GroupSum<G> sum(red);
-    const Cols<VEC, G, NV> c(threadIdx.x % G, p.dim);
-    float w[NV][VEC], sc[NV][VEC], dw[NV][VEC] = {}, ds[NV][VEC] = {};
-    load_cols<VEC, G, NV>(p.weight, p.weight_dtype, c, 1.f, w);
-    load_cols<VEC, G, NV>(p.scale_vec, p.scale_dtype, c, p.scale, sc);
+    const Cols<VEC, G, NV> c(p.dim);
+    const Weights<VEC, G, NV> weight(p.weight, p.weight_dtype, c, 1.f), scale(p.scale_vec, p.scale_dtype, c, p.scale);
+    Sums<VEC, G, NV> dw(shared), ds(shared + Sums<VEC, G, NV>::SHARED * blockDim.x);
     const float inv_dim = 1.f / (float)p.dim;
-    for (int64_t base = (int64_t)blockIdx.x * RPC; base < p.rows; base += (int64_t)gridDim.x * RPC) {
-        const uint32_t row = (uint32_t)base + threadIdx.x / G;
-        const bool live = row < p.rows;
-        const T *dy = reinterpret_cast<const T *>(p.dy) + (int64_t)row * p.dy_ts;
-        const T *x = reinterpret_cast<const T *>(p.x) + (int64_t)row * p.x_ts;
-        const R *r = reinterpret_cast<const R *>(p.residual_out) + (int64_t)row * p.ro_ts;
-        const R *dres = reinterpret_cast<const R *>(p.dres) + (int64_t)row * p.dres_ts;
-        float rv[NV][VEC], up[NV][VEC], s1 = 0.f, s2 = 0.f;
-        Pack<R, VEC> dr[NV] = {};
-        Pack<T, VEC> xp[NV] = {};
+    const int xo = X::N * 16 * blockDim.x, ro = 2 * xo, so = ro + Res::N * 16 * blockDim.x;
+    walk_rows<In, L::A, G, L::S, L::PLACES>(
+        p.rows, norm_smem,
+        [&](In &in, char *at, uint32_t row, bool live) {
+            in.dy.issue(at, p.dy, (int64_t)row * p.dy_ts, c, live);
+            in.r.issue(at + ro, p.residual_out, (int64_t)row * p.ro_ts, c, live);
+            in.dres.issue(at + so, p.dres, (int64_t)row * p.dres_ts, c, live && p.dres);
+            in.x.issue(at + xo, p.x, (int64_t)row * p.x_ts, c, live && p.dscale);
+        },
+        [&](const In &in, const char *at, uint32_t row, bool live) {
+            float r[NV][VEC], up[NV][VEC], s1 = 0.f, s2 = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            Pack<T, VEC> a = {};
-            Pack<R, VEC> b = {};
-            if (live && c.on[i]) {
-                a = load_pack<T, VEC>(dy + c.at(i));
-                b = load_pack<R, VEC>(r + c.at(i));
-                if (p.dres) dr[i] = load_pack<R, VEC>(dres + c.at(i));
-                if (p.dscale) xp[i] = load_pack<T, VEC>(x + c.at(i));
+            for (int i = 0; i < NV; ++i) {
+                float w[VEC];
+                weight.get(c, i, w);
+                in.dy.get(at, i, up[i]);
+                in.r.get(at + ro, i, r[i]);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    s1 = fmaf(r[i][j], r[i][j], s1);
+                    s2 = fmaf(up[i][j] * w[j], r[i][j], s2);
+                }
             }
-            unpack<T, VEC>(a, up[i]);
-            unpack<R, VEC>(b, rv[i]);
-        }
+            const float2 s = sum(s1, s2);
+            const float rs = rsqrtf(s.x * inv_dim + p.eps);
+            const NormGrad q(rs, s.y * inv_dim, p.dim, p.eps);
+            const int64_t o = (int64_t)row * p.dim;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                float d[VEC], x[VEC], w[VEC], sc[VEC];
+                weight.get(c, i, w);
+                scale.get(c, i, sc);
+                in.dres.get(at + so, i, d);
+                in.x.get(at + xo, i, x);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                s1 = fmaf(rv[i][j], rv[i][j], s1);
-                s2 = fmaf(up[i][j] * w[i][j], rv[i][j], s2);
+                for (int j = 0; j < VEC; ++j) {
+                    d[j] += q(up[i][j] * w[j], r[i][j]);
+                    dw.at(i, j) = fmaf(up[i][j], r[i][j] * rs, dw.at(i, j));
+                    ds.at(i, j) = fmaf(d[j], x[j], ds.at(i, j));
+                }
+                if (p.dresidual) store_piece<R>(p.dresidual, o, c, i, live, d);
+                if (p.dx) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) x[j] = sc[j] * d[j];
+                    store_piece<T>(p.dx, o, c, i, live, x);
+                }
             }
-        const float2 s = sum(s1, s2);
-        const float rs = rsqrtf(s.x * inv_dim + p.eps);
-        const NormGrad q(rs, s.y * inv_dim, p.dim, p.eps);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float d[VEC], dx[VEC], xv[VEC];
-            unpack<R, VEC>(dr[i], d);
-            unpack<T, VEC>(xp[i], xv);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                d[j] += q(up[i][j] * w[i][j], rv[i][j]);
-                dx[j] = sc[i][j] * d[j];
-                dw[i][j] = fmaf(up[i][j], rv[i][j] * rs, dw[i][j]);
-                ds[i][j] = fmaf(d[j], xv[j], ds[i][j]);
-            }
-            if (live && c.on[i]) {
-                const size_t o = (size_t)row * p.dim + c.at(i);
-                if (p.dresidual) store_pack<R, VEC>(reinterpret_cast<R *>(p.dresidual) + o, d);
-                if (p.dx) store_pack<T, VEC>(reinterpret_cast<T *>(p.dx) + o, dx);
-            }
-        }
-    }
+        });
     float *part = p.part + (size_t)blockIdx.x * p.dim;
-    if (p.dweight) write_part<VEC, G, NV>(part, psm, c, p.dim, dw);
+    if (p.dweight) write_part<VEC, G, NV>(part, shared, c, p.dim, dw);
     if (p.dweight) part += (size_t)gridDim.x * p.dim;
-    if (p.dscale) write_part<VEC, G, NV>(part, psm, c, p.dim, ds);
+    if (p.dscale) write_part<VEC, G, NV>(part, shared, c, p.dim, ds);
 }
 
-// ---------------------------------------------------------------- choice of the group
-// The fewest threads that hold a row in at most 4 pieces (16 single elements), up to 1024 threads.
-#define NORM_DISPATCH(T, vec, dim, CALL)                              \
-    do {                                                              \
-        if (vec) {                                                    \
-            constexpr int VE = 16 / (int)sizeof(T);                   \
-            const int n = (dim) / VE;                                 \
-            if (n <= 8) { CALL(VE, 8, 1); }                           \
-            else if (n <= 16) { CALL(VE, 16, 1); }                    \
-            else if (n <= 32) { CALL(VE, 32, 1); }                    \
-            else if (n <= 64) { CALL(VE, 32, 2); }                    \
-            else if (n <= 256) { CALL(VE, 128, 2); }                  \
-            else if (n <= 512) { CALL(VE, 256, 2); }                  \
-            else if (n <= 1024) { CALL(VE, 512, 2); }                 \
-            else if (n <= 2048) { CALL(VE, 512, 4); }                 \
-            else { CALL(VE, 1024, 4); }                               \
-        } else {                                                      \
-            if ((dim) <= 128) { CALL(1, 32, 4); }                     \
-            else if ((dim) <= 512) { CALL(1, 32, 16); }               \
-            else if ((dim) <= 2048) { CALL(1, 256, 8); }              \
-            else { CALL(1, 1024, 16); }                               \
-        }                                                             \
+// ---------------------------------------------------------------- choice of the row's threads
+// CALL(VEC, G, NV, most threads, threads): one piece to a thread up to 1024 threads, in whole warps.
+#define NORM_DISPATCH(T, vec, dim, CALL)                                                      \
+    do {                                                                                      \
+        if (vec) {                                                                            \
+            constexpr int VE = 16 / (int)sizeof(T);                                           \
+            const int n = (dim) / VE, up = (n + 31) / 32 * 32;                                \
+            if (n <= 8) { CALL(VE, 8, 1, NORM_THREADS, NORM_THREADS); }                       \
+            else if (n <= 16) { CALL(VE, 16, 1, NORM_THREADS, NORM_THREADS); }                \
+            else if (n <= 32) { CALL(VE, 32, 1, NORM_THREADS, NORM_THREADS); }                \
+            else if (n <= 256) { CALL(VE, 0, 1, 256, up); }                                   \
+            else if (n <= 512) { CALL(VE, 0, 1, 512, up); }                                   \
+            else if (n <= 1024) { CALL(VE, 0, 1, 1024, up); }                                 \
+            else if (n <= 2048) { CALL(VE, 0, 2, 1024, 1024); }                               \
+            else { CALL(VE, 0, VE == 4 ? 4 : 2, 1024, 1024); }                                \
+        } else {                                                                              \
+            if ((dim) <= 128) { CALL(1, 32, 4, NORM_THREADS, NORM_THREADS); }                 \
+            else if ((dim) <= 512) { CALL(1, 32, 16, NORM_THREADS, NORM_THREADS); }           \
+            else if ((dim) <= 2048) { CALL(1, 0, 8, 256, 256); }                              \
+            else { CALL(1, 0, 16, 1024, 1024); }                                              \
+        }                                                                                     \
     } while (0)
 
-// CTAs of a persistent grid: `threads_per_sm` threads on each of the device's SMs, no more than there are rows for.
-inline int norm_grid(int64_t rows, int threads, int rows_per_cta, int threads_per_sm, int most) {
-    int sms = 152;
-    if (device_sm_count(&sms) != cudaSuccess || sms < 1) sms = 152;
-    int64_t grid = (int64_t)sms * (threads_per_sm / threads > 0 ? threads_per_sm / threads : 1);
-    const int64_t need = (rows + rows_per_cta - 1) / rows_per_cta;
-    if (grid > need) grid = need;
-    if (grid > most) grid = most;
-    return (int)(grid < 1 ? 1 : grid);
+// Launches the persistent grid of a kernel; L says what shared memory it takes; grid: its number of CTAs, at most `most`.
+template <class L, class K, class P>
+cudaError_t norm_launch(K kernel, const P &p, int threads, int max_threads, int rows_per_cta, int most, int &grid,
+                        cudaStream_t stream) {
+    const int smem = L::bytes(threads);
+    cudaError_t e = norm_grid((const void *)kernel, threads, smem, L::bytes(max_threads), p.rows, rows_per_cta, most, grid);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, threads, smem, stream>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_colsum(const float *part, int parts, int dim, void *out, int dtype, cudaStream_t stream);
+cudaError_t launch_colsum(const float *part, int parts, int dim, int sums, void *out0, int dtype0, void *out1, int dtype1,
+                          cudaStream_t stream);
 
+// CTAs of an SM that a kernel is compiled for, of `threads` threads at most: 1024 threads in all; 2048 for the forward before a
+// block, which needs few registers (48763 x 4096 bf16 0.276 -> 0.258 ms); fewer for the backwards of single elements and for
+// the backward before a block with longer rows, whose column sums take them.
+constexpr int add_fwd_ctas(int residual_size, int vec, int pieces, int threads) {
+    return (residual_size == 4 || vec == 1 || pieces > 1 ? 1024 : 2048) / threads;
+}
+constexpr int add_bwd_ctas(int vec, int threads) { return threads > 256 ? 1 : vec == 1 ? 2 : 4; }
+constexpr int gated_bwd_ctas(int vec, int threads) { return vec > 1 ? 1024 / threads : threads > 256 ? 1 : 2; }
+#define NORM_ROWS(G) ((G) ? NORM_THREADS / ((G) ? (G) : 1) : 1)
 template <typename T> cudaError_t gated_norm_fwd_t(const GatedNormParams &p, cudaStream_t stream) {
-#define CALL(V, G, NV)                                                                                              \
-    k9_gated_fwd<T, V, G, NV><<<norm_grid(p.rows, norm_threads<V, G, NV>(), norm_threads<V, G, NV>() / G, 2048, 1 << 30), \
-                                norm_threads<V, G, NV>(), 0, stream>>>(p)
+    int grid = 0;
+#define CALL(V, G, NV, MAXT, threads)                                                                                  \
+    return norm_launch<GateFwd<T, V, G, NV>>(k9_gated_fwd<T, V, G, NV, MAXT, 1024 / MAXT>, p, threads, MAXT, NORM_ROWS(G), \
+                    1 << 30, grid, stream)
     NORM_DISPATCH(T, p.vec, p.dim, CALL);
 #undef CALL
-    return cudaGetLastError();
 }
 
 template <typename T> cudaError_t gated_norm_bwd_t(const GatedNormParams &p, cudaStream_t stream) {
-    const int most = norm_parts(p.rows, p.dim);
     int grid = 0;
-#define CALL(V, G, NV)                                                                                    \
-    grid = norm_grid(p.rows, norm_threads<V, G, NV>(), norm_threads<V, G, NV>() / G, 1024, most),         \
-    k9_gated_bwd<T, V, G, NV><<<grid, norm_threads<V, G, NV>(), 0, stream>>>(p)
+    cudaError_t e = cudaSuccess;
+#define CALL(V, G, NV, MAXT, threads)                                                                                  \
+    e = norm_launch<GateBwd<T, V, G, NV>>(k9_gated_bwd<T, V, G, NV, MAXT, gated_bwd_ctas(V, MAXT)>, p, threads, MAXT, NORM_ROWS(G), \
+                    norm_parts(p.rows, p.dim), grid, stream)
     NORM_DISPATCH(T, p.vec, p.dim, CALL);
 #undef CALL
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && p.dweight) e = launch_colsum(p.part, grid, p.dim, p.dweight, p.weight_dtype, stream);
-    return e;
+    if (e != cudaSuccess || !p.dweight) return e;
+    return launch_colsum(p.part, grid, p.dim, 1, p.dweight, p.weight_dtype, nullptr, 0, stream);
 }
 
 template <typename T, typename R> cudaError_t add_norm_fwd_t(const AddNormParams &p, cudaStream_t stream) {
-#define CALL(V, G, NV)                                                                                                \
-    k9_add_fwd<T, R, V, G, NV><<<norm_grid(p.rows, norm_threads<V, G, NV>(), norm_threads<V, G, NV>() / G, 2048, 1 << 30), \
-                                 norm_threads<V, G, NV>(), 0, stream>>>(p)
+    int grid = 0;
+#define CALL(V, G, NV, MAXT, threads)                                                                                  \
+    return norm_launch<AddFwd<T, R, V, G, NV>>(k9_add_fwd<T, R, V, G, NV, MAXT, add_fwd_ctas(sizeof(R), V, NV, MAXT)>, p, threads, MAXT, NORM_ROWS(G), \
+                    1 << 30, grid, stream)
     NORM_DISPATCH(T, p.vec, p.dim, CALL);
 #undef CALL
-    return cudaGetLastError();
 }
 
 template <typename T, typename R> cudaError_t add_norm_bwd_t(const AddNormParams &p, cudaStream_t stream) {
-    const int most = norm_parts(p.rows, p.dim);
     int grid = 0;
-#define CALL(V, G, NV)                                                                                    \
-    grid = norm_grid(p.rows, norm_threads<V, G, NV>(), norm_threads<V, G, NV>() / G, 1024, most),         \
-    k9_add_bwd<T, R, V, G, NV><<<grid, norm_threads<V, G, NV>(), 0, stream>>>(p)
+    cudaError_t e = cudaSuccess;
+#define CALL(V, G, NV, MAXT, threads)                                                                                  \
+    e = norm_launch<AddBwd<T, R, V, G, NV>>(k9_add_bwd<T, R, V, G, NV, MAXT, add_bwd_ctas(V, MAXT)>, p, threads, MAXT, NORM_ROWS(G), \
+                    norm_parts(p.rows, p.dim), grid, stream)
     NORM_DISPATCH(T, p.vec, p.dim, CALL);
 #undef CALL
-    cudaError_t e = cudaGetLastError();
-    const float *part = p.part;
-    if (e == cudaSuccess && p.dweight) {
-        e = launch_colsum(part, grid, p.dim, p.dweight, p.weight_dtype, stream);
-        part += (size_t)grid * p.dim;
-    }
-    if (e == cudaSuccess && p.dscale) e = launch_colsum(part, grid, p.dim, p.dscale, p.scale_dtype, stream);
-    return e;
+    const int sums = (p.dweight ? 1 : 0) + (p.dscale ? 1 : 0);
+    if (e != cudaSuccess || !sums) return e;
+    if (!p.dweight) return launch_colsum(p.part, grid, p.dim, 1, p.dscale, p.scale_dtype, nullptr, 0, stream);
+    return launch_colsum(p.part, grid, p.dim, sums, p.dweight, p.weight_dtype, p.dscale, p.scale_dtype, stream);
 }
 
 // what a translation unit instantiates for its activation type
