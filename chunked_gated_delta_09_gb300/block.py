@@ -46,9 +46,19 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+_entries = {}  # the library's functions by name, once it is loaded
+
+
+def _entry(name: str):
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(_lib.load(), name)
+    return fn
+
+
 def _queue(name: str, packed: bytes, index: int):
     """Call the C entry on torch's current stream of device ``index``."""
-    fn = getattr(_lib.load(), name)
+    fn = _entry(name)
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
             st = fn(packed, _raw_stream(index))
@@ -101,9 +111,11 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
 
 def _strides(t: torch.Tensor, name: str, inner: int):
     """(distance between tokens, distance between heads) of [..., heads, D] (inner = 2) or [..., D] (inner = 1)."""
-    shape, stride = t.shape, t.stride()
-    if t.numel() == 0:
-        return shape[-1] * (shape[-2] if inner == 2 else 1), shape[-1]
+    shape = t.shape
+    if t.is_contiguous():  # (so is a tensor without elements)
+        dim = shape[-1]
+        return (shape[-2] * dim, dim) if inner == 2 else (dim, dim)
+    stride = t.stride()
     _need(shape[-1] == 1 or stride[-1] == 1, f"{name}: the last axis must be contiguous")
     lead, step, span = None, 0, 1  # span: tokens covered by the axes seen so far
     for n, s in zip(reversed(shape[:-inner]), reversed(stride[:-inner])):
@@ -116,6 +128,13 @@ def _strides(t: torch.Tensor, name: str, inner: int):
                                     "distance (view them as one axis)")
         span *= n
     return step, (stride[-2] if inner == 2 else 0)
+
+
+def _result(x: torch.Tensor) -> torch.Tensor:
+    """An uninitialised contiguous tensor like x."""
+    if x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> int:
@@ -149,7 +168,7 @@ def gated_norm_fwd(x, z, weight, *, eps=1e-6, activation="silu", stream=None) ->
             return gated_norm_fwd(x, z, weight, eps=eps, activation=activation)
     index = _gated_check(x, z, weight, activation)
     heads, dim = x.shape[-2:]
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = _result(x)
     n = x.numel()
     if n == 0:
         return y
@@ -170,14 +189,14 @@ def gated_norm_bwd(dy, x, z, weight, *, eps=1e-6, activation="silu", stream=None
     _like(dy, "dy", index, x.shape, x.dtype)
     heads, dim = x.shape[-2:]
     dev = x.device
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dz = None if z is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dx = _result(x)
+    dz = None if z is None else _result(x)
     dw = None if weight is None else torch.empty(dim, dtype=weight.dtype, device=dev)
     n = x.numel()
     if n == 0:
         return dict(dx=dx, dz=dz, dweight=None if dw is None else dw.zero_())
     tokens = n // (heads * dim)
-    nbytes = 0 if dw is None else _lib.load().gdr_norm_workspace_bytes(tokens * heads, dim, 1)
+    nbytes = 0 if dw is None else _entry("gdr_norm_workspace_bytes")(tokens * heads, dim, 1)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     zs = (0, 0) if z is None else _strides(z, "z", 2)
     _queue("gdr_gated_norm_bwd",
@@ -247,8 +266,8 @@ def add_norm_fwd(x, residual, weight, scale=1.0, *, eps=1e-6, stream=None):
         _residual_type(residual, "residual", index, x)
     _vector(weight, "weight", index, dim)
     vec, num = _scale_of(scale, index, dim)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    out = torch.empty(x.shape, dtype=x.dtype if residual is None else residual.dtype, device=x.device)
+    y = _result(x)
+    out = _result(x if residual is None else residual)
     n = x.numel()
     if n == 0:
         return y, out
@@ -280,9 +299,9 @@ def add_norm_bwd(dy, dres, residual_out, weight, scale=1.0, *, x=None, eps=1e-6,
         _need(vec is not None, "x is for dscale: scale must be a tensor")
         _like(x, "x", index, dy.shape, dy.dtype)
     dev = dy.device
-    dr = torch.empty(dy.shape, dtype=residual_out.dtype, device=dev)
+    dr = _result(residual_out)
     same = vec is None and num == 1.0 and dr.dtype == dy.dtype
-    dx = dr if same else torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+    dx = dr if same else _result(dy)
     dw = None if weight is None else torch.empty(dim, dtype=weight.dtype, device=dev)
     ds = None if x is None else torch.empty(dim, dtype=vec.dtype, device=dev)
     out = dict(dx=dx, dresidual=dr, dweight=dw, dscale=ds)
@@ -293,7 +312,7 @@ def add_norm_bwd(dy, dres, residual_out, weight, scale=1.0, *, x=None, eps=1e-6,
                 t.zero_()
         return out
     sums = (dw is not None) + (ds is not None)
-    nbytes = _lib.load().gdr_norm_workspace_bytes(n // dim, dim, sums) if sums else 0
+    nbytes = _entry("gdr_norm_workspace_bytes")(n // dim, dim, sums) if sums else 0
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _queue("gdr_add_norm_bwd",
            _pack_add_bwd(dy.data_ptr(), _ptr(dres), residual_out.data_ptr(), _ptr(x), _ptr(weight), _ptr(vec),
@@ -350,7 +369,7 @@ def _linrec_check(x, g, h0, cu_seqlens):
 def _linrec_done(ws, check_status, index):
     if check_status:
         with torch.cuda.device(index):
-            st = _lib.load().gdr_linrec_get_status(ws.data_ptr(), _raw_stream(index))
+            st = _entry("gdr_linrec_get_status")(ws.data_ptr(), _raw_stream(index))
         if st:
             raise GdrError(st, "gdr_linrec_get_status")
 
@@ -370,11 +389,11 @@ def linrec_fwd(x, g, h0=None, cu_seqlens=None, *, complement=False, return_state
                               check_status=check_status)
     index, B, T, D, N = _linrec_check(x, g, h0, cu_seqlens)
     dev = x.device
-    h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    h = _result(x)
     ht = torch.empty(N, D, dtype=_F32, device=dev)
     tiles = -(-B * T // _lib.LINREC_SAVE)
     states = torch.empty(tiles, D, dtype=_F32, device=dev) if return_states else None
-    nbytes = _lib.load().gdr_linrec_workspace_bytes(B * T, D)
+    nbytes = _entry("gdr_linrec_workspace_bytes")(B * T, D)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _queue("gdr_linrec_fwd",
            _pack_linrec_fwd(x.data_ptr(), g.data_ptr(), _ptr(h0), _ptr(cu_seqlens), h.data_ptr(), ht.data_ptr(),
@@ -399,7 +418,7 @@ def linrec_bwd(x, g, dh, h0=None, dht=None, cu_seqlens=None, states=None, *, com
         _like(dht, "dht", index, (N, D), _F32)
         _need(dht.is_contiguous(), "dht must be contiguous")
     dev = x.device
-    nbytes = _lib.load().gdr_linrec_workspace_bytes(B * T, D)
+    nbytes = _entry("gdr_linrec_workspace_bytes")(B * T, D)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     tiles = -(-B * T // _lib.LINREC_SAVE)
     strides = _token_stride(x, "x"), _token_stride(g, "g")
@@ -413,8 +432,8 @@ def linrec_bwd(x, g, dh, h0=None, dht=None, cu_seqlens=None, states=None, *, com
     else:
         _like(states, "states", index, (tiles, D), _F32)
         _need(states.is_contiguous(), "states must be contiguous")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dg = torch.empty(x.shape, dtype=g.dtype, device=dev)
+    dx = _result(x)
+    dg = _result(g)
     dh0 = torch.empty(N, D, dtype=_F32, device=dev)
     _queue("gdr_linrec_bwd",
            _pack_linrec_bwd(x.data_ptr(), g.data_ptr(), dh.data_ptr(), _ptr(h0), _ptr(dht), states.data_ptr(),
@@ -468,7 +487,7 @@ def linrec_step(x, g, state, slots=None, *, complement=False, stream=None) -> to
         _need(slots.is_contiguous(), "slots must be contiguous")
     else:
         _need(state.shape[0] >= B, "state must have a row for each sequence")
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = _result(x)
     if B == 0 or D == 0:
         return y
     _queue("gdr_linrec_step",
@@ -479,32 +498,30 @@ def linrec_step(x, g, state, slots=None, *, complement=False, stream=None) -> to
 
 
 # ---------------------------------------------------------------- gradient norm and clip
+def _listed(tensors, name, index):
+    """Addresses, sizes and types of a list of tensors as arrays for the C entry."""
+    # (attribute by attribute: a list is checked in a fraction of the time that a loop over its tensors takes)
+    if [t.get_device() for t in tensors].count(index) != len(tensors) or not all([t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{name} must be contiguous tensors on cuda:{index}")
+    try:
+        types = array("i", [_DT[t.dtype] for t in tensors])
+    except KeyError:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16 tensors") from None
+    return array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors]), types
+
+
 def _clip(entry, grads: Sequence[torch.Tensor], max_norm, out, eps):
     grads = list(grads)
     _need(len(grads) > 0, "no gradients were given")
     index = _cuda(grads[0], "grads[0]")
-    ptrs, sizes, types = array("Q"), array("q"), array("i")
-    for i, t in enumerate(grads):
-        kind = _DT.get(t.dtype)
-        if kind is None or t.get_device() != index or not t.is_contiguous():
-            raise ValueError(f"grads[{i}] must be a contiguous float32, bfloat16 or float16 tensor on cuda:{index}")
-        ptrs.append(t.data_ptr())
-        sizes.append(t.numel())
-        types.append(kind)
+    ptrs, sizes, types = _listed(grads, "grads", index)
     outs, out_types = None, None
     if out is not None:
         out = list(out)
-        _need(len(out) == len(grads), "out must have one tensor for each gradient")
-        outs, out_types = array("Q"), array("i")
-        for i, (t, n) in enumerate(zip(out, sizes)):
-            kind = _DT.get(t.dtype)
-            if kind is None or t.get_device() != index or not t.is_contiguous() or t.numel() != n:
-                raise ValueError(f"out[{i}] must be a contiguous float32, bfloat16 or float16 tensor of grads[{i}]'s size "
-                                 f"on cuda:{index}")
-            outs.append(t.data_ptr())
-            out_types.append(kind)
+        outs, out_sizes, out_types = _listed(out, "out", index)
+        _need(out_sizes == sizes, "out must have one tensor for each gradient, of its size")
     dev = grads[0].device
-    nbytes = _lib.load().gdr_clip_workspace_bytes(len(grads), sum(sizes))
+    nbytes = _entry("gdr_clip_workspace_bytes")(len(grads), sum(sizes))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     norm = torch.empty((), dtype=_F32, device=dev)
 

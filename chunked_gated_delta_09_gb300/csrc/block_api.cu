@@ -392,6 +392,8 @@ static gdr_status clip_impl(const gdr_clip_args *a, bool scale, cudaStream_t str
             }
             t->first[t->count] = t->pieces;
             cudaError_t e = cudaSuccess;
+            if (pass == 0 && i == a->count && parts == 0 && clip_is_small(*t))
+                return done(launch_clip_small(*t, a->norm, scale, a->max_norm, a->eps, stream));
             if (pass == 0) {
                 if (t->pieces == 0) continue;
                 const int n = (int)(t->pieces < CLIP_CTAS ? t->pieces : CLIP_CTAS);

@@ -23,6 +23,10 @@ template <int N> struct ClipTable {
 static_assert(sizeof(ClipTable<CLIP_TENSORS>) <= 32000, "the table is a kernel argument");
 
 cudaError_t launch_clip_sumsq(const ClipTable<CLIP_TENSORS> &t, double *part, int parts, cudaStream_t stream);
+// Whether all tensors together are few enough for one launch, which then does everything.
+bool clip_is_small(const ClipTable<CLIP_TENSORS> &t);
+cudaError_t launch_clip_small(const ClipTable<CLIP_TENSORS> &t, float *norm, bool scale, float max_norm, float eps,
+                              cudaStream_t stream);
 cudaError_t launch_clip_norm(const double *part, int parts, float *norm, cudaStream_t stream);
 cudaError_t launch_clip_scale(const ClipTable<CLIP_TENSORS> &t, const double *part, int parts, float *norm, float max_norm,
                               float eps, cudaStream_t stream);

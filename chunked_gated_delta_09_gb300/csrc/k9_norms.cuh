@@ -186,15 +186,28 @@ __device__ __forceinline__ void store_piece(void *p, int64_t at, const Cols<VEC,
     if (live && c.on[i]) store_pack<T, VEC>(reinterpret_cast<T *>(p) + at + c.at(i), x);
 }
 
-// The CTA's column sums to its partial row: the rows' threads are added in order, in `smem` that nothing else uses by then.
+// Where a CTA's column sums go: its partial row, or the result itself where it is the only CTA.
+struct ColumnSums {
+    float *part;
+    void *out;
+    int dtype;
+    __device__ __forceinline__ ColumnSums(float *p, void *o, int dt, int which, int dim)
+        : part(p + ((size_t)which * gridDim.x + blockIdx.x) * dim), out(o), dtype(dt) {}
+    __device__ __forceinline__ void put(int col, float x) const {
+        if (gridDim.x == 1) store_scalar(out, col, x, dtype);
+        else part[col] = x;
+    }
+};
+// The rows' threads are added in order, in `smem` that nothing else uses by then.
 template <int VEC, int G, int NV>
-__device__ __forceinline__ void write_part(float *part, float *smem, const Cols<VEC, G, NV> &c, int dim, Sums<VEC, G, NV> &acc) {
+__device__ __forceinline__ void write_sums(const ColumnSums &to, float *smem, const Cols<VEC, G, NV> &c, int dim,
+                                           Sums<VEC, G, NV> &acc) {
     if constexpr (G == 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (c.on[i])
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) part[c.at(i) + j] = acc.at(i, j);
+                for (int j = 0; j < VEC; ++j) to.put(c.at(i) + j, acc.at(i, j));
     } else {
         constexpr int W = G * NV * VEC, RPC = NORM_THREADS / G;  // columns held by a row's threads
         const int gi = threadIdx.x / G;
@@ -207,7 +220,7 @@ __device__ __forceinline__ void write_part(float *part, float *smem, const Cols<
         for (int col = threadIdx.x; col < dim; col += NORM_THREADS) {
             float s = 0.f;
             for (int r = 0; r < RPC; ++r) s += smem[r * W + col];
-            part[col] = s;
+            to.put(col, s);
         }
     }
 }
@@ -377,7 +390,7 @@ __device__ __forceinline__ void gated_bwd(const GatedNormParams &p, char *ring, 
                 if (ACT != ACT_NONE) store_piece<T>(p.dz, o, c, i, live, dz[i]);
             }
         });
-    if (p.dweight) write_part<VEC, G, NV>(p.part + (size_t)blockIdx.x * p.dim, shared, c, p.dim, dw);
+    if (p.dweight) write_sums<VEC, G, NV>({p.part, p.dweight, p.weight_dtype, 0, p.dim}, shared, c, p.dim, dw);
 }
 
 template <typename T, int VEC, int G, int NV, int MAXT, int MINB>
@@ -528,10 +541,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k9_add_bwd(const __grid_constant__
                 }
             }
         });
-    float *part = p.part + (size_t)blockIdx.x * p.dim;
-    if (p.dweight) write_part<VEC, G, NV>(part, shared, c, p.dim, dw);
-    if (p.dweight) part += (size_t)gridDim.x * p.dim;
-    if (p.dscale) write_part<VEC, G, NV>(part, shared, c, p.dim, ds);
+    if (p.dweight) write_sums<VEC, G, NV>({p.part, p.dweight, p.weight_dtype, 0, p.dim}, shared, c, p.dim, dw);
+    if (p.dscale) write_sums<VEC, G, NV>({p.part, p.dscale, p.scale_dtype, p.dweight ? 1 : 0, p.dim}, shared, c, p.dim, ds);
 }
 
 // ---------------------------------------------------------------- choice of the row's threads
@@ -556,6 +567,10 @@ __global__ void __launch_bounds__(MAXT, MINB) k9_add_bwd(const __grid_constant__
             else { CALL(1, 0, 16, 1024, 1024); }                                              \
         }                                                                                     \
     } while (0)
+
+// CTAs of a backward that sums columns, at most.  Few rows take one, which writes the sums itself: a row in turn costs it about
+// 1 us, a second launch 2 us on the device and 8 us on the host where the device waits for it.
+inline int sum_ctas(int64_t rows, int rows_per_cta, int dim) { return rows <= 4 * rows_per_cta ? 1 : norm_parts(rows, dim); }
 
 // Launches the persistent grid of a kernel; L says what shared memory it takes; grid: its number of CTAs, at most `most`.
 template <class L, class K, class P>
@@ -596,10 +611,10 @@ template <typename T> cudaError_t gated_norm_bwd_t(const GatedNormParams &p, cud
     cudaError_t e = cudaSuccess;
 #define CALL(V, G, NV, MAXT, threads)                                                                                  \
     e = norm_launch<GateBwd<T, V, G, NV>>(k9_gated_bwd<T, V, G, NV, MAXT, gated_bwd_ctas(V, MAXT)>, p, threads, MAXT, NORM_ROWS(G), \
-                    norm_parts(p.rows, p.dim), grid, stream)
+                    sum_ctas(p.rows, NORM_ROWS(G), p.dim), grid, stream)
     NORM_DISPATCH(T, p.vec, p.dim, CALL);
 #undef CALL
-    if (e != cudaSuccess || !p.dweight) return e;
+    if (e != cudaSuccess || !p.dweight || grid == 1) return e;
     return launch_colsum(p.part, grid, p.dim, 1, p.dweight, p.weight_dtype, nullptr, 0, stream);
 }
 
@@ -617,11 +632,11 @@ template <typename T, typename R> cudaError_t add_norm_bwd_t(const AddNormParams
     cudaError_t e = cudaSuccess;
 #define CALL(V, G, NV, MAXT, threads)                                                                                  \
     e = norm_launch<AddBwd<T, R, V, G, NV>>(k9_add_bwd<T, R, V, G, NV, MAXT, add_bwd_ctas(V, MAXT)>, p, threads, MAXT, NORM_ROWS(G), \
-                    norm_parts(p.rows, p.dim), grid, stream)
+                    sum_ctas(p.rows, NORM_ROWS(G), p.dim), grid, stream)
     NORM_DISPATCH(T, p.vec, p.dim, CALL);
 #undef CALL
     const int sums = (p.dweight ? 1 : 0) + (p.dscale ? 1 : 0);
-    if (e != cudaSuccess || !sums) return e;
+    if (e != cudaSuccess || !sums || grid == 1) return e;
     if (!p.dweight) return launch_colsum(p.part, grid, p.dim, 1, p.dscale, p.scale_dtype, nullptr, 0, stream);
     return launch_colsum(p.part, grid, p.dim, sums, p.dweight, p.weight_dtype, p.dscale, p.scale_dtype, stream);
 }
