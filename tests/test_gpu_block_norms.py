@@ -201,3 +201,40 @@ def test_another_stream():
     y = gated_norm_fwd(x, z, w, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(y, ref)
+
+
+def test_rows_beyond_32_bits():
+    """More than 2^31 elements: the last rows are those of a call on them alone."""
+    n, dim, tail = 140000, 16384, 9
+    gen = torch.Generator("cuda").manual_seed(18)
+    x = torch.empty(n, dim, device="cuda", dtype=torch.bfloat16)
+    x[-tail:] = torch.randn(tail, dim, generator=gen, device="cuda").bfloat16()
+    x[:-tail] = 1.0
+    w = torch.ones(dim, device="cuda")
+    y, r = add_norm_fwd(x, x, w, 0.5)
+    ref_y, ref_r = add_norm_fwd(x[-tail:], x[-tail:], w, 0.5)
+    assert torch.equal(y[-tail:], ref_y) and torch.equal(r[-tail:], ref_r)
+    assert torch.equal(gated_norm_fwd(x[:, None], x[:, None], w)[-tail:, 0], gated_norm_fwd(x[-tail:, None], x[-tail:, None], w)[:, 0])
+
+
+@pytest.mark.parametrize("rows", [1, 4, 5, 64, 65, 130])
+def test_column_sums_of_few_rows(rows):
+    """Around the numbers of rows up to which one CTA writes the sums itself."""
+    gen = U.seeded(rows)
+    for dim in (64, 128, 700, 2048):
+        x, res, dy, dres = (U.randn(gen, rows, dim, dtype=torch.bfloat16) for _ in range(4))
+        check_add(x, res, 1.0 + U.randn(gen, dim, times=0.2), 0.5 + U.randn(gen, dim, times=0.2), dy, dres)
+        check_gated(x[:, None], res[:, None], 1.0 + U.randn(gen, dim, times=0.2), dy[:, None], "silu")
+
+
+def test_capture_in_a_graph():
+    gen = U.seeded(19)
+    x, z, dy = (U.randn(gen, 2000, 4, 64, dtype=torch.bfloat16) for _ in range(3))
+    w = U.randn(gen, 64)
+    ref = gated_norm_bwd(dy, x, z, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = gated_norm_bwd(dy, x, z, w)
+    graph.replay()
+    assert all(torch.equal(got[k], ref[k]) for k in ref)

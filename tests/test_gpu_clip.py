@@ -112,3 +112,19 @@ def test_capture_in_a_graph():
     n = norm64(grads)
     assert abs(float(norm) - n) <= U.FP32_BAR * n
     assert all(U.rel(o, U.f64(t) / (n + 1e-6)) <= U.FP32_BAR for o, t in zip(out, grads))
+
+
+@pytest.mark.parametrize("pieces", [31, 32, 33])
+def test_around_the_largest_single_launch(pieces):
+    gen = U.seeded(pieces)
+    check([U.randn(gen, 16384 * (pieces - 3) + 5), U.randn(gen, 3, dtype=torch.bfloat16), U.randn(gen, 100)], 1.0)
+
+
+def test_a_tensor_beyond_32_bits():
+    n = (1 << 31) + 70000
+    g = torch.full((n,), 0.5, device="cuda", dtype=torch.bfloat16)
+    g[-3:] = torch.tensor([1.0, 2.0, -4.0], device="cuda").bfloat16()
+    norm = clip_grad_norm([g], 1.0)
+    ref = ((n - 3) * 0.25 + 21.0) ** 0.5
+    assert abs(float(norm) - ref) <= U.FP32_BAR * ref
+    assert U.rel(g[-3:], torch.tensor([1.0, 2.0, -4.0], dtype=torch.float64) / (ref + 1e-6)) <= U.BAR[torch.bfloat16]

@@ -190,3 +190,80 @@ def test_step_of_nothing():
     x = torch.ones(2, 16, device="cuda")
     y = linrec_step(x, x, state, torch.tensor([-1, -1], dtype=torch.int32, device="cuda"))
     assert not y.any() and torch.equal(state, torch.ones_like(state))
+
+
+# ---------------------------------------------------------------- many channels, many sequences, long rows
+@pytest.mark.parametrize("T,D", [(3000, 1000), (700, 4100), (257, 10008), (5000, 520), (1025, 96)])
+def test_blocks_of_channels(T, D):
+    """Widths whose blocks of 32 channels fill several waves of clusters, or end inside a block."""
+    p, d = problem(1, T, D, "bf16", "f32", seed=T)
+    check(p, d, None, True)
+
+
+def test_many_sequences():
+    gen = torch.Generator().manual_seed(21)
+    lens = torch.randint(0, 4, (2500,), generator=gen).tolist()
+    p, d = problem(1, sum(lens), 40, "f32", "f32", seed=22, lens=lens)
+    check(p, d, lens, False)
+
+
+def test_rows_beyond_32_bits():
+    """More than 2^31 elements: the last rows, whose sequence starts late, against the same sequence by itself."""
+    T, D, tail = (1 << 20) + 5000, 2056, 700
+    gen = torch.Generator("cuda").manual_seed(23)
+    x = torch.randn(1, T, D, generator=gen, device="cuda", dtype=torch.bfloat16)
+    g = torch.full((1, T, D), -0.05, device="cuda", dtype=torch.bfloat16)
+    g[:, -tail:] = -torch.rand(1, tail, D, generator=gen, device="cuda").bfloat16()
+    cu = torch.tensor([0, T - tail, T], dtype=torch.int32, device="cuda")
+    h, ht, states = linrec_fwd(x, g, None, cu, return_states=True, check_status=True)
+    ref, ref_ht = linrec_fwd(x[:, -tail:].contiguous(), g[:, -tail:].contiguous())
+    assert U.rel(h[:, -tail:], U.f64(ref)) <= 1e-3 and U.rel(ht[1:], U.f64(ref_ht)) <= U.FP32_BAR
+    dh = x
+    got = linrec_bwd(x, g, dh, None, None, cu, states)
+    alone = linrec_bwd(x[:, -tail:].contiguous(), g[:, -tail:].contiguous(), dh[:, -tail:].contiguous())
+    assert U.rel(got["dx"][:, -tail:], U.f64(alone["dx"])) <= 1e-3
+    assert U.rel(got["dg"][:, -tail:], U.f64(alone["dg"])) <= 1e-3
+    assert U.rel(got["dh0"][1:], U.f64(alone["dh0"])) <= U.FP32_BAR
+
+
+def test_large_and_small_gates():
+    """Decays that underflow, that are 1, and that grow."""
+    g = torch.tensor([0.0, -1e-6, -87.0, -88.5, -200.0, float("-inf"), 0.5, 3.0, -0.35, -0.34], device="cuda")
+    g = g.repeat(8, 4)[None].contiguous()
+    x = U.randn(U.seeded(24), *g.shape)
+    p = dict(x=x, g=g, h0=U.randn(U.seeded(25), 1, 40), cu_seqlens=None)
+    check(p, dict(dh=U.randn(U.seeded(26), *g.shape), dht=U.randn(U.seeded(27), 1, 40)), None, True)
+
+
+def test_waits_that_run_out_are_reported(monkeypatch):
+    """With a limit of one poll real waits run out: the call reports it, ends in order, and the next call is right."""
+    p, _ = problem(1, 6000, 256, "bf16", "f32", seed=28)
+    ref = linrec_fwd(p["x"], p["g"], p["h0"])
+    monkeypatch.setenv("GDR_SPIN_LIMIT", "1")
+    statuses = []
+    for _ in range(3):
+        try:
+            h, ht = linrec_fwd(p["x"], p["g"], p["h0"], check_status=True)
+            statuses.append(_lib.GDR_OK)
+        except GdrError as e:
+            statuses.append(e.status)
+    assert _lib.GDR_ERR_TIMEOUT in statuses and set(statuses) <= {_lib.GDR_OK, _lib.GDR_ERR_TIMEOUT}, statuses
+    monkeypatch.delenv("GDR_SPIN_LIMIT")
+    again = linrec_fwd(p["x"], p["g"], p["h0"], check_status=True)
+    assert all(torch.equal(a, b) for a, b in zip(ref, again))
+
+
+def test_capture_in_a_graph_and_other_streams():
+    p, d = problem(1, 900, 96, "bf16", "bf16", seed=29, lens=[300, 600])
+    ref = linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"])
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(out, ref))
