@@ -35,11 +35,8 @@ static_assert(LR_SAVE == LR_BWD_GROUPS / LR_WARPS * LR_R, "a saved state enters 
 // remembers hundreds of tokens would add up (decays near 1 that come out a quarter of a unit too low put h off by
 // 1e-5).  Cody and Waite's reduction g = n ln 2 + r, then exp(r) - 1 = r + r^2 q(r) with q a Chebyshev fit of degree 4
 // (1e-8 off), so that 1 - a is exact to rounding near a = 1.  Below -87.7 a is 0; above 88.3 it is taken at 88.3.
-__device__ __forceinline__ void decay2(float g0, float g1, F2 &a, F2 &rest) {
-    const float lo = -88.f, hi = 88.3f;
-    asm("min.NaN.f32 %0, %0, %1;\n\tmax.NaN.f32 %0, %0, %2;" : "+f"(g0) : "f"(hi), "f"(lo));
-    asm("min.NaN.f32 %0, %0, %1;\n\tmax.NaN.f32 %0, %0, %2;" : "+f"(g1) : "f"(hi), "f"(lo));
-    const F2 g(g0, g1), shift(12582912.f), one(1.f);  // 1.5 x 2^23: the sum's low bits are the rounded integer
+__device__ __forceinline__ void decay2(F2 g, F2 &a, F2 &rest) {
+    const F2 shift(12582912.f), one(1.f);  // 1.5 x 2^23: the sum's low bits are the rounded integer
     const F2 t = fma2(g, F2(1.44269504f), shift), n = add2(t, F2(-12582912.f));
     const F2 r = fma2(n, F2(-0.693147181f), g);  // (ln 2 is 1.9e-9 off: n times that, below a rounding of a until a < 1e-9)
     F2 q = fma2(r, F2(0.0013933823f), F2(0.0083632953f));
@@ -54,6 +51,25 @@ __device__ __forceinline__ void decay2(float g0, float g1, F2 &a, F2 &rest) {
     a = fma2(p, s, s);
     const F2 ns = mul2(s, F2(-1.f));
     rest = fma2(p, ns, add2(one, ns));
+}
+
+// Two gates as they lie in memory, taken to [-88, 88] (16-bit types: both by one instruction) or [-88, 88.3]; a nan stays one.
+__device__ __forceinline__ F2 gates(Pack<float, 2> g) {
+    const float lo = -88.f, hi = 88.3f;
+    asm("min.NaN.f32 %0, %0, %1;\n\tmax.NaN.f32 %0, %0, %2;" : "+f"(g.v[0]) : "f"(hi), "f"(lo));
+    asm("min.NaN.f32 %0, %0, %1;\n\tmax.NaN.f32 %0, %0, %2;" : "+f"(g.v[1]) : "f"(hi), "f"(lo));
+    return F2(g.v[0], g.v[1]);
+}
+__device__ __forceinline__ F2 gates(Pack<__nv_bfloat16, 2> g) {
+    uint32_t v = *reinterpret_cast<uint32_t *>(&g);
+    asm("min.NaN.bf16x2 %0, %0, %1;\n\tmax.NaN.bf16x2 %0, %0, %2;" : "+r"(v) : "r"(0x42b042b0u), "r"(0xc2b0c2b0u));
+    return F2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ F2 gates(Pack<__half, 2> g) {
+    uint32_t v = *reinterpret_cast<uint32_t *>(&g);
+    asm("min.NaN.f16x2 %0, %0, %1;\n\tmax.NaN.f16x2 %0, %0, %2;" : "+r"(v) : "r"(0x55805580u), "r"(0xd580d580u));
+    const __half2 h = *reinterpret_cast<__half2 *>(&v);
+    return F2(__low2float(h), __high2float(h));
 }
 
 // Four neighbouring channels of a row.
@@ -333,13 +349,18 @@ __device__ __forceinline__ F4 row4(const float *p, int64_t row, int c, int dim) 
 }
 
 // Sequences without a token have no row: their last state is their first (forward), their gradients pass through
-// (backward).  The tiles share them out; by one warp.
-__device__ __forceinline__ void empty_sequences(const LinrecParams &p, int64_t tile, int cb, const float *from, float *to) {
-    if ((!p.cu && p.tokens > 0) || !to || tile >= p.tiles) return;
-    const int64_t lo = p.N * tile / p.tiles, hi = p.N * (tile + 1) / p.tiles;
-    const int c = cb * LR_CH + (threadIdx.x & 31);
-    for (int64_t s = lo; s < hi; ++s)
-        if (c < p.dim && (!p.cu || p.cu[s] == p.cu[s + 1])) to[s * p.dim + c] = from ? from[s * p.dim + c] : 0.f;
+// (backward).  The cluster's warps share out the sequences of its block of channels.
+__device__ __forceinline__ void empty_sequences(const LinrecParams &p, int rank, int cb, const float *from, float *to) {
+    if ((!p.cu && p.tokens > 0) || !to) return;
+    const int lane = threadIdx.x & 31, c = cb * LR_CH + lane;
+    for (int base = 32 * (rank * LR_WARPS + (int)(threadIdx.x >> 5)); base < p.N; base += 32 * LR_WARPS * p.cluster) {
+        const int s = base + lane;
+        uint32_t empty = __ballot_sync(0xffffffffu, s < p.N && (!p.cu || p.cu[s] == p.cu[s + 1]));
+        for (; empty; empty &= empty - 1) {
+            const int64_t at = (int64_t)(base + __ffs(empty) - 1) * p.dim + c;
+            if (c < p.dim) to[at] = from ? from[at] : 0.f;
+        }
+    }
 }
 
 // cu_seqlens that do not rise from 0 to the number of rows are reported; the grid shares the check.
@@ -417,6 +438,8 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
     cluster_sync();  // the barriers are there, everywhere
     for (int k = 0; k < S && k < p.supers; ++k)
         if (!VEC || threadIdx.x == 0) fetch(k);
+    __syncwarp();
+    empty_sequences(p, rank, cb, p.h0, p.ht);
     float walked = 0.f;  // (warp 1) the state that enters the cluster's rows
     for (int k = 0; k < p.supers; ++k) {
         const int buf = k & 1, tile = k * p.cluster + rank, first = group * R, row0 = tile * ROWS + first;
@@ -431,11 +454,10 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
         auto compose = [&](auto any) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float g[4];
-                gt.get(first + r, ch, g);
+                const Pack<G, 4> g = *reinterpret_cast<const Pack<G, 4> *>(&gt.v[first + r][ch]);
                 F4 rest;
-                decay2(g[0], g[1], a[r].lo, rest.lo);
-                decay2(g[2], g[3], a[r].hi, rest.hi);
+                decay2(gates(*reinterpret_cast<const Pack<G, 2> *>(&g.v[0])), a[r].lo, rest.lo);
+                decay2(gates(*reinterpret_cast<const Pack<G, 2> *>(&g.v[2])), a[r].hi, rest.hi);
                 b[r] = xt.get4(first + r, ch);
                 if (COMP) b[r] = mul4(b[r], rest);
                 if (any.value && (heads >> r) & 1) {
@@ -461,7 +483,6 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
             sm.carry[lane] = sm.peers.entry(buf, rank, p.cluster, walked);
         } else if (wid == 2) {
             if (k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile + p.cluster, sa, sb);
-            empty_sequences(p, tile, cb, p.h0, p.ht);
         }
         __syncthreads();
         F4 h = through<LR_GROUPS>(sm.maps, group, ch, cuts & ((1u << group) - 1), sm.carry);
@@ -545,6 +566,8 @@ __global__ void __launch_bounds__(LR_THREADS, 3)
         fetch_x(0);
         if (p.supers > 1) fetch_g(1);
     }
+    __syncwarp();
+    empty_sequences(p, rank, cb, p.dht, p.dh0);
     float walked = 0.f;
     for (int k = 0; k < p.supers; ++k) {
         const int buf = k & 1, tile = tile_of(k), first = group * R, row0 = tile * ROWS + first;
@@ -572,7 +595,7 @@ __global__ void __launch_bounds__(LR_THREADS, 3)
             for (int r = 0; r < R; ++r) {
                 const Pack<G, 2> g = *reinterpret_cast<const Pack<G, 2> *>(&gt.v[first + r][ch]);
                 F2 u;
-                decay2(to_f32(g.v[0]), to_f32(g.v[1]), a[r], u);
+                decay2(gates(g), a[r], u);
                 F2 b = xt.get2(first + r, ch);
                 if (COMP) rest[r] = u, b = mul2(b, u);
                 if (any.value && (heads >> r) & 1) B = fma2(a[r], row2(p.h0, ends.sequence_of(p, row0 + r), c, p.dim), b);
@@ -613,7 +636,6 @@ __global__ void __launch_bounds__(LR_THREADS, 3)
             sm.carry[lane] = sm.peers.entry(buf, rank, p.cluster, walked);
         } else if (wid == 2) {
             if (k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile - p.cluster, sa, sb);
-            empty_sequences(p, tile, cb, p.dht, p.dh0);
         }
         __syncthreads();
         F2 m = through2(&sm.maps[wid][ch], tcuts & ((1u << (LR_WARPS - 1 - wid)) - 1), &sm.carry[ch]);
@@ -671,7 +693,7 @@ template <typename T, typename G, int V, bool COMP> __global__ void __launch_bou
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             F2 a, rest;
-            decay2(g[j], g[j], a, rest);
+            decay2(gates(Pack<float, 2>{g[j], g[j]}), a, rest);
             float a0, a1, r0, r1;
             a.get(a0, a1);
             rest.get(r0, r1);
