@@ -99,9 +99,13 @@ enum class Ahead { NONE, PAIR, RING };
 // (fp32 beside 16-bit types) is copied by the lanes of the row's part in the order of memory, so that each instruction
 // covers whole sectors.
 template <typename T, int VEC, int G, int NV, Ahead A> struct Feed {
+    static constexpr bool LATE = A == Ahead::NONE && NV * VEC > 8;  // read where it is used: registers would not hold it
     static constexpr int N = A == Ahead::RING ? VEC * (int)sizeof(T) / 16 : 0;  // 16-byte places of a thread
     static constexpr int L = G ? G : 32;                                        // lanes that copy for each other
-    Pack<T, VEC> v[A == Ahead::RING ? 1 : NV];
+    Pack<T, VEC> v[A == Ahead::RING || LATE ? 1 : NV];
+    const T *row;
+    const Cols<VEC, G, NV> *cols;
+    bool live_;
     static __device__ __forceinline__ int place_of(int chunk) {  // (lanes that read two each hit different banks)
         return 16 * (N == 2 ? chunk ^ ((chunk >> 3) & 1) : chunk);
     }
@@ -114,6 +118,8 @@ template <typename T, int VEC, int G, int NV, Ahead A> struct Feed {
                 const bool on = live && col < c.dim;
                 copy16(place + place_of(first * N + chunk), reinterpret_cast<const T *>(p) + (on ? at + col : 0), on);
             }
+        } else if constexpr (LATE) {
+            row = reinterpret_cast<const T *>(p) + at, cols = &c, live_ = live;
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -128,6 +134,10 @@ template <typename T, int VEC, int G, int NV, Ahead A> struct Feed {
 #pragma unroll
             for (int k = 0; k < N; ++k)
                 reinterpret_cast<uint4 *>(&a)[k] = *reinterpret_cast<const uint4 *>(place + place_of(threadIdx.x * N + k));
+            unpack<T, VEC>(a, o);
+        } else if constexpr (LATE) {
+            Pack<T, VEC> a = {};
+            if (live_ && cols->on[i]) a = load_pack<T, VEC>(row + cols->at(i));
             unpack<T, VEC>(a, o);
         } else {
             unpack<T, VEC>(v[i], o);
@@ -144,7 +154,7 @@ constexpr int norm_ahead(int places, int budget = 12) {
 // The weights of a thread's columns, in registers unless it has several pieces, and its column sums, which then lie in
 // places of its own in shared memory.
 template <int VEC, int G, int NV> struct Weights {
-    static constexpr bool KEPT = NV * VEC <= 8 || VEC == 1;
+    static constexpr bool KEPT = NV * VEC <= 8;
     const void *p;
     int dt;
     float fill, v[KEPT ? NV : 1][KEPT ? VEC : 1];
@@ -164,7 +174,7 @@ template <int VEC, int G, int NV> struct Weights {
     }
 };
 template <int VEC, int G, int NV> struct Sums {
-    static constexpr bool KEPT = NV * VEC <= 8 || VEC == 1;
+    static constexpr bool KEPT = NV * VEC <= 8;
     static constexpr int SHARED = KEPT ? 0 : NV * VEC;  // floats of a thread
     float v[KEPT ? NV : 1][KEPT ? VEC : 1];
     float *s;
@@ -561,9 +571,12 @@ __global__ void __launch_bounds__(MAXT, MINB) k9_add_bwd(const __grid_constant__
             else if (n <= 2048) { CALL(VE, 0, 2, 1024, 1024); }                               \
             else { CALL(VE, 0, VE == 4 ? 4 : 2, 1024, 1024); }                                \
         } else {                                                                              \
+            const int up = ((dim) + 63) / 64 * 32;                                            \
             if ((dim) <= 128) { CALL(1, 32, 4, NORM_THREADS, NORM_THREADS); }                 \
-            else if ((dim) <= 512) { CALL(1, 32, 16, NORM_THREADS, NORM_THREADS); }           \
-            else if ((dim) <= 2048) { CALL(1, 0, 8, 256, 256); }                              \
+            else if ((dim) <= 512) { CALL(1, 0, 2, 256, up); }                                \
+            else if ((dim) <= 1024) { CALL(1, 0, 2, 512, up); }                               \
+            else if ((dim) <= 2048) { CALL(1, 0, 2, 1024, up); }                              \
+            else if ((dim) <= 4096) { CALL(1, 0, 4, 1024, 1024); }                            \
             else { CALL(1, 0, 16, 1024, 1024); }                                              \
         }                                                                                     \
     } while (0)
@@ -589,13 +602,12 @@ cudaError_t launch_colsum(const float *part, int parts, int dim, int sums, void 
                           cudaStream_t stream);
 
 // CTAs of an SM that a kernel is compiled for, of `threads` threads at most: 1024 threads in all; 2048 for the forward before a
-// block, which needs few registers (48763 x 4096 bf16 0.276 -> 0.258 ms); fewer for the backwards of single elements and for
-// the backward before a block with longer rows, whose column sums take them.
+// block, which needs few registers (48763 x 4096 bf16 0.276 -> 0.258 ms); 512 for the backward before a block with longer
+// rows, whose column sums take them.
 constexpr int add_fwd_ctas(int residual_size, int vec, int pieces, int threads) {
     return (residual_size == 4 || vec == 1 || pieces > 1 ? 1024 : 2048) / threads;
 }
-constexpr int add_bwd_ctas(int vec, int threads) { return threads > 256 ? 1 : vec == 1 ? 2 : 4; }
-constexpr int gated_bwd_ctas(int vec, int threads) { return vec > 1 ? 1024 / threads : threads > 256 ? 1 : 2; }
+constexpr int add_bwd_ctas(int vec, int threads) { return threads <= 256 || vec == 1 ? 1024 / threads : 1; }
 #define NORM_ROWS(G) ((G) ? NORM_THREADS / ((G) ? (G) : 1) : 1)
 template <typename T> cudaError_t gated_norm_fwd_t(const GatedNormParams &p, cudaStream_t stream) {
     int grid = 0;
@@ -610,7 +622,7 @@ template <typename T> cudaError_t gated_norm_bwd_t(const GatedNormParams &p, cud
     int grid = 0;
     cudaError_t e = cudaSuccess;
 #define CALL(V, G, NV, MAXT, threads)                                                                                  \
-    e = norm_launch<GateBwd<T, V, G, NV>>(k9_gated_bwd<T, V, G, NV, MAXT, gated_bwd_ctas(V, MAXT)>, p, threads, MAXT, NORM_ROWS(G), \
+    e = norm_launch<GateBwd<T, V, G, NV>>(k9_gated_bwd<T, V, G, NV, MAXT, 1024 / MAXT>, p, threads, MAXT, NORM_ROWS(G), \
                     sum_ctas(p.rows, NORM_ROWS(G), p.dim), grid, stream)
     NORM_DISPATCH(T, p.vec, p.dim, CALL);
 #undef CALL
