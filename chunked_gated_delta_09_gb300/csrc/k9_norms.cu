@@ -54,10 +54,14 @@ __global__ void __launch_bounds__(1024) k9_colsum(const float *part, int parts, 
     part += (size_t)blockIdx.y * parts * dim;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before has ended, its partial rows are there
     float a = 0.f;
-    if (col < dim) {
-#pragma unroll 8
-        for (int r = wid; r < parts; r += 32) a += part[(size_t)r * dim + col];
-    }
+    if (col < dim)
+        for (int r0 = wid; r0 < parts; r0 += 32 * 10) {
+            float v[10];  // all under way at once
+#pragma unroll
+            for (int i = 0; i < 10; ++i) v[i] = r0 + 32 * i < parts ? part[(size_t)(r0 + 32 * i) * dim + col] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 10; ++i) a += v[i];
+        }
     s[wid][lane] = a;
     __syncthreads();
     if (wid == 0 && col < dim) {

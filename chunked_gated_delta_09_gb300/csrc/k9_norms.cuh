@@ -332,10 +332,18 @@ __device__ __forceinline__ void gated_fwd(const GatedNormParams &p, char *ring) 
                 float y[VEC], z[VEC], w[VEC];
                 weight.get(c, i, w);
                 if (ACT != ACT_NONE) in.z.get(at + zo, i, z);
+                if constexpr (VEC > 1) {  // two values to an instruction
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    y[j] = x[i][j] * rs * w[j];
-                    if (ACT != ACT_NONE) y[j] *= ACT == 0 ? z[j] * sigmoid_t<T>(z[j]) : sigmoid_t<T>(z[j]);
+                    for (int j = 0; j < VEC; j += 2) {
+                        F2 v = mul2(mul2(F2(x[i][j], x[i][j + 1]), F2(rs)), F2(w[j], w[j + 1]));
+                        if (ACT != ACT_NONE) v = mul2(v, F2(sigmoid_t<T>(z[j]), sigmoid_t<T>(z[j + 1])));
+                        if (ACT == 0) v = mul2(v, F2(z[j], z[j + 1]));
+                        v.get(y[j], y[j + 1]);
+                    }
+                } else {
+                    y[0] = x[i][0] * rs * w[0];
+                    if (ACT != ACT_NONE) y[0] *= sigmoid_t<T>(z[0]);
+                    if (ACT == 0) y[0] *= z[0];
                 }
                 store_piece<T>(p.y, (int64_t)row * p.dim, c, i, live, y);
             }
