@@ -223,15 +223,17 @@ struct Peers {
 // Which rows of a tile are the first or the last of a sequence.
 template <int ROWS> struct Ends {
     static constexpr int R = LR_R;
-    uint32_t head[ROWS / 32], tail[ROWS / 32];  // a bit for each row
+    uint32_t head[ROWS / 32], tail[ROWS / 32];  // a bit for each row; written where there is any
+    bool any;
     // by one warp; [a, b): the sequence that the warp met last, with which it goes on
     __device__ __forceinline__ void find(const LinrecParams &p, int tile, int &a, int &b) {
         const int lane = threadIdx.x & 31, row0 = tile * ROWS, end = min(row0 + ROWS, p.rows);
         if (row0 < p.rows && !(a <= row0 && row0 < b)) sequence_of(p, row0, a, b);
         if (row0 >= p.rows || (a < row0 && b > end)) {  // the tile lies within one sequence, or has no rows
-            if (lane < ROWS / 32) head[lane] = tail[lane] = 0;
+            if (lane == 0) any = false;
             return;
         }
+        if (lane == 0) any = true;
         for (int k = 0; k < ROWS / 32; ++k) {
             const int row = row0 + 32 * k + lane;
             int from = -1, to = -1;
@@ -446,9 +448,13 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
         const Ends<ROWS> &ends = sm.ends[buf];
         const auto &gt = st.g[k % S];
         const auto &xt = st.x[k % S];
-        const uint32_t cuts = ends.head_cuts(), heads = ends.heads(group), tails = ends.tails(group);
         // as a rule every row and channel is there, and no sequence starts or ends among the warp's rows
-        const bool plain = channels && (tile + 1) * ROWS <= p.rows && !__any_sync(0xffffffffu, heads | tails);
+        bool plain = channels && (tile + 1) * ROWS <= p.rows;
+        uint32_t cuts = 0, heads = 0, tails = 0;
+        if (ends.any) {
+            cuts = ends.head_cuts(), heads = ends.heads(group), tails = ends.tails(group);
+            plain = plain && !__any_sync(0xffffffffu, heads | tails);
+        }
         if (VEC) wait_phase(&sm.full[k % S], (k / S) & 1, p);
         F4 a[R], b[R], A, B;
         auto compose = [&](auto any) {
@@ -574,8 +580,12 @@ __global__ void __launch_bounds__(LR_THREADS, 3)
         const Ends<ROWS> &ends = sm.ends[buf];
         const auto &gt = st.g[buf];
         const auto &xt = st.x[buf], &dt = st.dh[buf];
-        const uint32_t tcuts = ends.tail_cuts(), heads = ends.heads(group), tails = ends.tails(group);
-        const bool plain = channels && (tile + 1) * ROWS <= p.rows && !__any_sync(0xffffffffu, heads | tails);
+        bool plain = channels && (tile + 1) * ROWS <= p.rows;
+        uint32_t tcuts = 0, heads = 0, tails = 0;
+        if (ends.any) {
+            tcuts = ends.tail_cuts(), heads = ends.heads(group), tails = ends.tails(group);
+            plain = plain && !__any_sync(0xffffffffu, heads | tails);
+        }
         const int warp0 = tile * ROWS + wid * LR_SAVE;  // the warp's first row
         // the h that enters it
         F2 h = plain ? *reinterpret_cast<const F2 *>(p.states + (int64_t)(warp0 / LR_SAVE) * p.dim + c)
