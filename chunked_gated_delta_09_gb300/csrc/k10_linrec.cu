@@ -60,8 +60,8 @@ cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, cud
     p.per_seq = FastDiv::of((uint32_t)(p.tokens > 0 ? p.tokens : 1));
     const int64_t nblk = (p.dim + LR_CH - 1) / LR_CH;
     // The size whose clusters take the fewest tiles one after the other, all waves of them together.  A tile takes about 2 %
-    // longer with each CTA more, from the exchange of the maps (backward at 48763 x 4096 bf16: 3 CTAs, 127 tiles in turn,
-    // 0.539 ms; 10 CTAs, 117 tiles, 0.567 ms; 4 CTAs in two waves, 192 tiles, 0.592 ms).
+    // longer with each CTA more, from the exchange of the maps (48763 x 4096 bf16, backward: 6 CTAs, 127 tiles in turn,
+    // 0.501 ms; 5 CTAs, 153 tiles, 0.529 ms; 10 CTAs in two waves, 154 tiles, 0.521 ms; 7 CTAs in two, 218, 0.590 ms).
     int64_t best = -1;
     for (int size = 1; size <= LR_MAX_CLUSTER; ++size) {
         if (r.clusters[size] < 1 || size > p.tiles) continue;

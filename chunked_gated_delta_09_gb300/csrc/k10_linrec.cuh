@@ -26,9 +26,9 @@ using tc::mbar_expect_tx;
 using tc::mbar_init;
 using tc::mbar_wait;
 
-constexpr int LR_WARPS = 8, LR_THREADS = 32 * LR_WARPS;
+constexpr int LR_WARPS = 4, LR_THREADS = 32 * LR_WARPS;
 constexpr int LR_R = 8;                        // rows of a group
-constexpr int LR_GROUPS = 32, LR_BWD_GROUPS = 16;  // groups of a tile, 4 (backwards 2) to a warp
+constexpr int LR_GROUPS = 16, LR_BWD_GROUPS = 8;  // groups of a tile, 4 (backwards 2) to a warp
 static_assert(LR_SAVE == LR_BWD_GROUPS / LR_WARPS * LR_R, "a saved state enters each warp's rows of the backward");
 
 // exp(g) and 1 - exp(g), both to about one unit in the last place and without a lean to one side, which a channel that
@@ -99,8 +99,8 @@ template <int W> __device__ __forceinline__ void put_maps(Maps<W> &at, int w, in
 // and composes over distances 1, 2, 4 ...; bit j of cuts: the map at position j cuts off what came before.
 template <int W, bool BACK>
 __device__ __forceinline__ void scan_maps(Maps<W> &maps, uint32_t cuts, int wid, int lane, float2 *total) {
-    constexpr int N = W / 8;  // channels of a lane
-    const int j = lane % W, ch = 4 * wid + lane / W;
+    constexpr int N = W / LR_WARPS;  // channels of a lane
+    const int j = lane % W, ch = LR_CH / LR_WARPS * wid + N * (lane / W);
     float2 *at = &maps[BACK ? W - 1 - j : j][ch];
     float a[N], b[N];
 #pragma unroll
@@ -187,24 +187,24 @@ struct Peers {
     float2 map[2][LR_MAX_CLUSTER][LR_CH];
     int cut[2][LR_MAX_CLUSTER];
     uint64_t bar[2];
-    // by one warp: this CTA's map, a lane for each channel, to all
-    __device__ __forceinline__ void tell(int buf, int rank, int size, float2 m, bool c) {
-        const int lane = threadIdx.x & 31;
-        if (lane == 0) mbar_expect_tx(&bar[buf], (uint32_t)size * (LR_CH * 8 + 4));
+    // by every warp, which has its channels of `total`: this CTA's map to all
+    __device__ __forceinline__ void tell(int buf, int rank, int size, const float2 *total, bool c) {
+        constexpr int PER = LR_CH / LR_WARPS;  // channels of a warp
+        const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, ch = PER * wid + lane % PER;
+        __syncwarp();
+        if (threadIdx.x == 32) mbar_expect_tx(&bar[buf], (uint32_t)size * (LR_CH * 8 + 4));
         uint64_t v;
-        asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(m.x), "f"(m.y));
-        for (int q = 0; q < size; ++q) {
-            const uint32_t b = in_cta(&bar[buf], q);
+        asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(total[ch].x), "f"(total[ch].y));
+        for (int q = lane / PER; q < size; q += 32 / PER)
             asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
-                             in_cta(&map[buf][rank][lane], q)),
-                         "l"(v), "r"(b)
+                             in_cta(&map[buf][rank][ch], q)),
+                         "l"(v), "r"(in_cta(&bar[buf], q))
                          : "memory");
-            if (lane == 0)
-                asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
-                                 in_cta(&cut[buf][rank], q)),
-                             "r"((int)c), "r"(b)
-                             : "memory");
-        }
+        if (wid == 0 && lane < size)
+            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                             in_cta(&cut[buf][rank], lane)),
+                         "r"((int)c), "r"(in_cta(&bar[buf], lane))
+                         : "memory");
     }
     // For a lane's channel, the state s that enters the cluster's rows taken through the tiles before that of CTA `rank`;
     // s itself is taken through all of them.
@@ -268,7 +268,11 @@ template <int ROWS> struct Ends {
     __device__ __forceinline__ uint32_t heads(int g) const { return head[g * R / 32] >> (g * R % 32) & ((1u << R) - 1); }
     __device__ __forceinline__ uint32_t tails(int g) const { return tail[g * R / 32] >> (g * R % 32) & ((1u << R) - 1); }
     // bit per group: a sequence starts among its rows
-    __device__ __forceinline__ uint32_t head_cuts() const { return __ballot_sync(0xffffffffu, heads(threadIdx.x & 31)); }
+    __device__ __forceinline__ uint32_t head_cuts() const {
+        constexpr int N = ROWS / R;  // groups
+        static_assert(N < 32 && (N & (N - 1)) == 0, "a lane for each group");
+        return __ballot_sync(0xffffffffu, heads(threadIdx.x & (N - 1))) & ((1u << N) - 1);
+    }
     // bit per warp, from the last one on: a sequence ends among its rows
     __device__ __forceinline__ uint32_t tail_cuts() const {
         const int w = LR_WARPS - 1 - (threadIdx.x & (LR_WARPS - 1)), n = ROWS / LR_WARPS;
@@ -375,13 +379,6 @@ __device__ __forceinline__ void check_sequences(const LinrecParams &p) {
     if (bad) atomicOr(p.status, ST_BAD_SEQLENS);
 }
 
-// The warps' parts of the tile's map are in shared memory: the others say so and go on, the one that needs them waits.
-__device__ __forceinline__ void totals_there(bool wait) {
-    __syncwarp();
-    if (wait) asm volatile("bar.sync 1, %0;" ::"n"(LR_THREADS) : "memory");
-    else asm volatile("bar.arrive 1, %0;" ::"n"(LR_THREADS) : "memory");
-}
-
 // What the two kernels have in common: a CTA's shared memory besides the stages.
 template <int ROWS, int S, int W> struct LinrecSmem {
     Maps<W> maps;
@@ -403,14 +400,14 @@ __device__ __forceinline__ void init_barriers(uint64_t *full, int stages, Peers 
 
 // ---------------------------------------------------------------- forward
 template <typename T, typename G> struct FwdStages {
-    static constexpr int ROWS = LR_R * LR_GROUPS, S = 2;
+    static constexpr int ROWS = LR_R * LR_GROUPS, S = 1;
     static constexpr uint32_t BYTES = sizeof(Tile<G, ROWS>) + sizeof(Tile<T, ROWS>);
     Tile<G, ROWS> g[S];
     Tile<T, ROWS> x[S];
 };
 
 template <typename T, typename G, bool COMP, bool VEC>
-__global__ void __launch_bounds__(LR_THREADS, 2)
+__global__ void __launch_bounds__(LR_THREADS, 5)
     k10_fwd(const __grid_constant__ LinrecParams p, const __grid_constant__ LinrecMaps maps) {
     using Stages = FwdStages<T, G>;
     constexpr int R = LR_R, ROWS = Stages::ROWS, S = Stages::S;
@@ -480,11 +477,10 @@ __global__ void __launch_bounds__(LR_THREADS, 2)
         put_maps<LR_GROUPS>(sm.maps, group, ch, A, B);
         __syncthreads();
         // the tile's rows are in registers: their place takes the tile S further on
-        if (k + S < p.supers && (!VEC || threadIdx.x == 128)) fetch(k + S);
+        if (k + S < p.supers && (!VEC || threadIdx.x == 96)) fetch(k + S);
         scan_maps<LR_GROUPS, false>(sm.maps, cuts, wid, lane, sm.total);
-        totals_there(wid == 1);
+        sm.peers.tell(buf, rank, p.cluster, sm.total, cuts != 0);
         if (wid == 1) {
-            sm.peers.tell(buf, rank, p.cluster, sm.total[lane], cuts != 0);
             wait_peers(&sm.peers.bar[buf], (k >> 1) & 1, p);
             sm.carry[lane] = sm.peers.entry(buf, rank, p.cluster, walked);
         } else if (wid == 2) {
@@ -527,7 +523,7 @@ template <typename T, typename G> struct BwdStages {
 };
 
 template <typename T, typename G, bool COMP, bool VEC>
-__global__ void __launch_bounds__(LR_THREADS, 3)
+__global__ void __launch_bounds__(LR_THREADS, 6)
     k10_bwd(const __grid_constant__ LinrecParams p, const __grid_constant__ LinrecMaps maps) {
     using Stages = BwdStages<T, G>;
     constexpr int R = LR_R, ROWS = Stages::ROWS;
@@ -633,15 +629,14 @@ __global__ void __launch_bounds__(LR_THREADS, 3)
         const F2 out = shfl2(heads ? B : fma2(A, h, B), lane & 15);
         if (lane >= 16) h = out;
         __syncthreads();
+        scan_maps<LR_WARPS, true>(sm.maps, tcuts, wid, lane, sm.total);
+        sm.peers.tell(buf, rank, p.cluster, sm.total, tcuts != 0);
         // everybody is done with this tile's g and with x and dh of the tile before
-        if (!VEC || threadIdx.x == 128) {
+        if (!VEC || threadIdx.x == 96) {
             if (k + 1 < p.supers) fetch_x(k + 1);
             if (k + 2 < p.supers) fetch_g(k + 2);
         }
-        scan_maps<LR_WARPS, true>(sm.maps, tcuts, wid, lane, sm.total);
-        totals_there(wid == 1);
         if (wid == 1) {
-            sm.peers.tell(buf, rank, p.cluster, sm.total[lane], tcuts != 0);
             wait_peers(&sm.peers.bar[buf], (k >> 1) & 1, p);
             sm.carry[lane] = sm.peers.entry(buf, rank, p.cluster, walked);
         } else if (wid == 2) {
