@@ -80,60 +80,64 @@ __device__ __forceinline__ F4 fma4(F4 a, F4 b, F4 c) { return {fma2(a.lo, b.lo, 
 __device__ __forceinline__ F4 mul4(F4 a, F4 b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
 __device__ __forceinline__ F4 add4(F4 a, F4 b) { return {add2(a.lo, b.lo), add2(a.hi, b.hi)}; }
 __device__ __forceinline__ F4 make4(float x, float y, float z, float w) { return {F2(x, y), F2(z, w)}; }
-__device__ __forceinline__ F4 make4(const float4 &v) { return make4(v.x, v.y, v.z, v.w); }
 
 // ---------------------------------------------------------------- maps
-// The maps of W groups (or warps).  Rows of 33 put the lanes of a scan on different banks.
-template <int W> using Maps = float2[W][LR_CH + 1];
+// The maps of W groups (or warps).  Rows of 34 put the lanes of a scan on different banks and each pair of maps on 16 bytes.
+template <int W> using Maps = float2[W][LR_CH + 2];
 
-template <int W> __device__ __forceinline__ void put_maps(Maps<W> &at, int w, int ch, F4 a, F4 b) {
+__device__ __forceinline__ void put_pair(float2 *at, F2 a, F2 b) {
     float x, y, u, v;
-    a.lo.get(x, y), b.lo.get(u, v);
-    at[w][ch] = make_float2(x, u), at[w][ch + 1] = make_float2(y, v);
-    a.hi.get(x, y), b.hi.get(u, v);
-    at[w][ch + 2] = make_float2(x, u), at[w][ch + 3] = make_float2(y, v);
+    a.get(x, y), b.get(u, v);
+    *reinterpret_cast<float4 *>(at) = make_float4(x, u, y, v);
+}
+__device__ __forceinline__ void get_pair(const float2 *at, F2 &a, F2 &b) {
+    const float4 m = *reinterpret_cast<const float4 *>(at);
+    a = F2(m.x, m.z), b = F2(m.y, m.w);
 }
 
 // Composes W maps along the scan (from the last to the first with BACK): in place each becomes the map of the rows before
-// it, and `total` that of all of them.  A warp takes 4 channels, W / 8 to a lane, a lane for each position of the scan,
-// and composes over distances 1, 2, 4 ...; bit j of cuts: the map at position j cuts off what came before.
-template <int W, bool BACK>
+// it, and `total` that of all of them.  A warp takes 8 channels, four lanes to each, a quarter of the positions to a lane:
+// it composes them in turn, the lanes' maps over distances 1 and 2, and its own again from what comes before them; bit j
+// of cuts: the map at position j cuts off what came before.
+template <int W, bool BACK, bool CUTS>
 __device__ __forceinline__ void scan_maps(Maps<W> &maps, uint32_t cuts, int wid, int lane, float2 *total) {
-    constexpr int N = W / LR_WARPS;  // channels of a lane
-    const int j = lane % W, ch = LR_CH / LR_WARPS * wid + N * (lane / W);
-    float2 *at = &maps[BACK ? W - 1 - j : j][ch];
-    float a[N], b[N];
+    constexpr int N = W / 4;  // positions of a lane
+    static_assert(LR_WARPS * 8 == LR_CH && W % 4 == 0, "four lanes to a channel");
+    const int part = lane >> 3, ch = 8 * wid + (lane & 7);
+    auto at = [&](int i) -> float2 & { return maps[BACK ? W - 1 - part * N - i : part * N + i][ch]; };
+    float2 m[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) a[i] = at[i].x, b[i] = at[i].y;
+    for (int i = 0; i < N; ++i) m[i] = at(i);
+    auto add = [&](float2 first, int i) {  // the map of position i after that of the rows before it
+        const bool cut = CUTS && (cuts >> (part * N + i)) & 1;
+        return make_float2(m[i].x * first.x, cut ? m[i].y : fmaf(m[i].x, first.y, m[i].y));
+    };
+    float2 own = m[0];
 #pragma unroll
-    for (int d = 1; d < W; d *= 2) {
-        const bool cut = cuts && (cuts >> ((j - d + 1) & 31)) & ((1u << d) - 1);
+    for (int i = 1; i < N; ++i) own = add(own, i);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float a1 = __shfl_up_sync(0xffffffffu, a[i], d, W), b1 = __shfl_up_sync(0xffffffffu, b[i], d, W);
-            if (j >= d) {
-                if (!cut) b[i] = fmaf(a[i], b1, b[i]);
-                a[i] *= a1;
-            }
+    for (int d = 1; d < 4; d *= 2) {
+        const float a1 = __shfl_up_sync(0xffffffffu, own.x, 8 * d), b1 = __shfl_up_sync(0xffffffffu, own.y, 8 * d);
+        if (part >= d) {
+            const bool cut = CUTS && (cuts >> ((part - d + 1) * N)) & ((1u << (d * N)) - 1);
+            if (!cut) own.y = fmaf(own.x, b1, own.y);
+            own.x *= a1;
         }
     }
+    if (part == 3) total[ch] = own;
+    float2 before = make_float2(__shfl_up_sync(0xffffffffu, own.x, 8), __shfl_up_sync(0xffffffffu, own.y, 8));
+    if (part == 0) before = make_float2(1.f, 0.f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        if (j == W - 1) total[ch + i] = make_float2(a[i], b[i]);
-        const float a1 = __shfl_up_sync(0xffffffffu, a[i], 1, W), b1 = __shfl_up_sync(0xffffffffu, b[i], 1, W);
-        at[i] = j ? make_float2(a1, b1) : make_float2(1.f, 0.f);
+        at(i) = before;
+        if (i + 1 < N) before = add(before, i);
     }
 }
-// Four channels' states taken through the map that scan_maps left; cut: that map cuts off.
-template <int W> __device__ __forceinline__ F4 through(const Maps<W> &maps, int w, int ch, bool cut, const float *s) {
-    const float2 *m = &maps[w][ch];
-    const float2 m0 = m[0], m1 = m[1], m2 = m[2], m3 = m[3];
-    const F4 b = make4(m0.y, m1.y, m2.y, m3.y);
-    return cut ? b : fma4(make4(m0.x, m1.x, m2.x, m3.x), make4(*reinterpret_cast<const float4 *>(s + ch)), b);
-}
-__device__ __forceinline__ F2 through2(const float2 *m, bool cut, const float *s) {
-    const F2 b(m[0].y, m[1].y);
-    return cut ? b : fma2(F2(m[0].x, m[1].x), F2(s[0], s[1]), b);
+// Two channels' states taken through a map that scan_maps left; cut: that map cuts off.
+__device__ __forceinline__ F2 through(const float2 *m, bool cut, const float *s) {
+    F2 a, b;
+    get_pair(m, a, b);
+    return cut ? b : fma2(a, F2(s[0], s[1]), b);
 }
 __device__ __forceinline__ F2 shfl2(F2 v, int lane) {
     float x, y;
@@ -381,7 +385,7 @@ __device__ __forceinline__ void check_sequences(const LinrecParams &p) {
 
 // What the two kernels have in common: a CTA's shared memory besides the stages.
 template <int ROWS, int S, int W> struct LinrecSmem {
-    Maps<W> maps;
+    alignas(16) Maps<W> maps;
     Peers peers;
     float2 total[LR_CH];          // the tile's map
     float carry[LR_CH];           // what enters the tile
@@ -474,11 +478,13 @@ __global__ void __launch_bounds__(LR_THREADS, 5)
         };
         if (plain) compose(Const<false>());
         else compose(Const<true>());
-        put_maps<LR_GROUPS>(sm.maps, group, ch, A, B);
+        put_pair(&sm.maps[group][ch], A.lo, B.lo);
+        put_pair(&sm.maps[group][ch + 2], A.hi, B.hi);
         __syncthreads();
         // the tile's rows are in registers: their place takes the tile S further on
         if (k + S < p.supers && (!VEC || threadIdx.x == 96)) fetch(k + S);
-        scan_maps<LR_GROUPS, false>(sm.maps, cuts, wid, lane, sm.total);
+        if (cuts) scan_maps<LR_GROUPS, false, true>(sm.maps, cuts, wid, lane, sm.total);
+        else scan_maps<LR_GROUPS, false, false>(sm.maps, cuts, wid, lane, sm.total);
         sm.peers.tell(buf, rank, p.cluster, sm.total, cuts != 0);
         if (wid == 1) {
             wait_peers(&sm.peers.bar[buf], (k >> 1) & 1, p);
@@ -487,7 +493,8 @@ __global__ void __launch_bounds__(LR_THREADS, 5)
             if (k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile + p.cluster, sa, sb);
         }
         __syncthreads();
-        F4 h = through<LR_GROUPS>(sm.maps, group, ch, cuts & ((1u << group) - 1), sm.carry);
+        const bool cut = cuts & ((1u << group) - 1);
+        F4 h = {through(&sm.maps[group][ch], cut, &sm.carry[ch]), through(&sm.maps[group][ch + 2], cut, &sm.carry[ch + 2])};
         if (p.states && first % LR_SAVE == 0 && row0 < p.rows)
             put4<VEC>(p.states + (int64_t)(row0 / LR_SAVE) * p.dim + c, h, c, p.dim);
         T *to = reinterpret_cast<T *>(p.h) + (int64_t)row0 * p.dim + c;
@@ -619,17 +626,13 @@ __global__ void __launch_bounds__(LR_THREADS, 6)
         // backward: the second group's map for the lanes of the first, which leave the warp's
         const uint32_t ended = __ballot_sync(0xffffffffu, tails);
         const F2 A1 = shfl2(A, lane | 16), Q1 = shfl2(Q, lane | 16);
-        if (lane < 16) {
-            float x, y, u, v;
-            mul2(A, A1).get(x, y);
-            (tails ? Q : fma2(A, Q1, Q)).get(u, v);
-            sm.maps[wid][ch] = make_float2(x, u), sm.maps[wid][ch + 1] = make_float2(y, v);
-        }
+        if (lane < 16) put_pair(&sm.maps[wid][ch], mul2(A, A1), tails ? Q : fma2(A, Q1, Q));
         // forward: what leaves the first group enters the second
         const F2 out = shfl2(heads ? B : fma2(A, h, B), lane & 15);
         if (lane >= 16) h = out;
         __syncthreads();
-        scan_maps<LR_WARPS, true>(sm.maps, tcuts, wid, lane, sm.total);
+        if (tcuts) scan_maps<LR_WARPS, true, true>(sm.maps, tcuts, wid, lane, sm.total);
+        else scan_maps<LR_WARPS, true, false>(sm.maps, tcuts, wid, lane, sm.total);
         sm.peers.tell(buf, rank, p.cluster, sm.total, tcuts != 0);
         // everybody is done with this tile's g and with x and dh of the tile before
         if (!VEC || threadIdx.x == 96) {
@@ -643,7 +646,7 @@ __global__ void __launch_bounds__(LR_THREADS, 6)
             if (k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile - p.cluster, sa, sb);
         }
         __syncthreads();
-        F2 m = through2(&sm.maps[wid][ch], tcuts & ((1u << (LR_WARPS - 1 - wid)) - 1), &sm.carry[ch]);
+        F2 m = through(&sm.maps[wid][ch], tcuts & ((1u << (LR_WARPS - 1 - wid)) - 1), &sm.carry[ch]);
         if (lane < 16) m = ended >> 16 ? Q1 : fma2(A1, m, Q1);
         auto finish = [&](auto any) {
             F2 before[R];  // h_{t-1}, less x_t with COMP
