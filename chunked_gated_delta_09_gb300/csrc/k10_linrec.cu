@@ -61,12 +61,14 @@ cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, cud
     const int64_t nblk = (p.dim + LR_CH - 1) / LR_CH;
     // The size whose clusters take the fewest tiles one after the other, all waves of them together.  A tile takes about 2 %
     // longer with each CTA more, from the exchange of the maps (48763 x 4096 bf16, backward: 6 CTAs, 127 tiles in turn,
-    // 0.501 ms; 5 CTAs, 153 tiles, 0.529 ms; 10 CTAs in two waves, 154 tiles, 0.521 ms; 7 CTAs in two, 218, 0.590 ms).
+    // 0.404 ms; 5 CTAs, 153 tiles, 0.426 ms; 10 CTAs in two waves, 154 tiles, 0.432 ms; 7 CTAs in two, 218, 0.497 ms); a wave
+    // has to start and to end, which costs it about two more (4096 x 8192 bf16, forward: 2 CTAs in one wave, 16 tiles, 0.051
+    // ms; 8 CTAs in three, 12 tiles, 0.056 ms).
     int64_t best = -1;
     for (int size = 1; size <= LR_MAX_CLUSTER; ++size) {
         if (r.clusters[size] < 1 || size > p.tiles) continue;
         const int64_t waves = (nblk + r.clusters[size] - 1) / r.clusters[size];
-        const int64_t cost = waves * ((p.tiles + size - 1) / size) * (50 + size);
+        const int64_t cost = waves * ((p.tiles + size - 1) / size + 2) * (50 + size);
         if (best < 0 || cost < best) best = cost, p.cluster = size;
     }
     p.supers = (p.tiles + p.cluster - 1) / p.cluster;
