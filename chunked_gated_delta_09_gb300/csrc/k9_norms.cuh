@@ -6,9 +6,13 @@
 //     t = dy w ;  dr = rs t - r rs^3 mean(t r) + dres ;  dx = s dr ;  dw = sum of dy r rs ;  ds = sum of dr x
 //
 // Both row sums of a backward (of squares and of t x) come from one pass over values that stay in registers, so
-// every input is read once and every output written once: the kernels are bound by HBM.  A row belongs to 8, 16 or 32
-// lanes or to a whole CTA, a thread holding one piece of VEC elements where the row fits 1024 threads.  Lanes sum by
-// shuffles, CTAs through shared memory.  The grid is persistent: the weights are read once per thread, and the column sums
+// every input is read once and every output written once: the kernels are bound by HBM, which a plain copy moves at
+// 6.8 TB/s.  After a block, 32768 x 16 x 128 bf16: forward 0.064 ms (6.3 TB/s), backward 0.126 ms with its column sums (5.3
+// TB/s; instructions are issued in 79 % of the cycles, the activation and its derivative for every element).  Before one:
+// forward 48763 x 4096 bf16 0.252 ms (6.3), backward 0.309 (6.5); 32768 x 2048 bf16 on an fp32 stream 0.134 (6.0), backward
+// with the gradient of the scale 0.198 (6.1).  Few rows take the time of a launch.  A row belongs to 8, 16 or 32 lanes or to
+// a whole CTA, a thread holding one piece of VEC elements where the row fits 1024 threads.  Lanes sum by shuffles, CTAs
+// through shared memory.  The grid is persistent: the weights are read once per thread, and the column sums
 // of a backward (dw, ds) stay in registers until the CTA writes its partial row, which k9_colsum adds in a fixed order.
 // The rows ahead come in one of three ways (see Ahead), whichever measured fastest for the kernel.
 #pragma once
@@ -87,12 +91,14 @@ template <int G> __device__ __forceinline__ int cta_row() { return G ? threadIdx
 
 // How the rows ahead come.
 //   RING   by asynchronous copies to places in shared memory, several rows ahead, which takes no registers: the backward
-//          kernels (32768 x 16 x 128 bf16 after a block 0.125 ms; PAIR 0.136; 48763 x 4096 bf16 before one 0.309; PAIR 0.425),
-//          and the forward before a block on a 16-bit stream (48763 x 4096 0.253 ms; PAIR 0.271)
+//          kernels (32768 x 16 x 128 bf16 after a block 0.126 ms; PAIR 0.143; 48763 x 4096 bf16 before one 0.309; PAIR 0.484),
+//          and the forward before a block on a 16-bit stream (48763 x 4096 0.252 ms; PAIR 0.271)
 //   PAIR   the next row's pieces in registers while a row is worked on: the forward after a block (32768 x 16 x 128 bf16
-//          0.066 ms; RING 0.070), and before one on an fp32 stream (32768 x 2048 0.127; RING 0.140)
-//   NONE   a row's pieces when it is its turn, other CTAs covering the wait: single elements and rows of several pieces to a
-//          thread, which leave no registers (20000 x 1001 fp32 stream, backward 0.117 ms; PAIR 0.144)
+//          0.064 ms; RING 0.072), before one on an fp32 stream (32768 x 2048 0.134; RING 0.141), and before one by single
+//          elements, up to 4 to a thread (20000 x 1001 fp32 stream, backward 0.088 ms; NONE 0.135)
+//   NONE   a row's pieces when it is its turn, other CTAs covering the wait: rows of several pieces to a thread, for which
+//          there are no registers (4000 x 16384 fp32 stream, backward 0.368 ms; PAIR 0.712), and after a block single
+//          elements too (20000 x 1001 forward 0.049 ms, backward 0.089; PAIR 0.063, 0.094)
 enum class Ahead { NONE, PAIR, RING };
 
 // How a thread gets its pieces of a row of one tensor; zeros where there is nothing.  In a RING a piece of two 16-byte places
@@ -144,7 +150,11 @@ template <typename T, int VEC, int G, int NV, Ahead A> struct Feed {
         }
     }
 };
-template <int VEC, int NV> constexpr Ahead ahead_or_none(Ahead a) { return VEC == 1 || NV > 1 ? Ahead::NONE : a; }
+// (single elements always come in several pieces)
+template <int NV> constexpr Ahead ahead_or_none(Ahead a) { return NV > 1 ? Ahead::NONE : a; }
+template <int VEC, int NV> constexpr Ahead before_block(Ahead a) {
+    return VEC == 1 && NV <= 4 ? Ahead::PAIR : ahead_or_none<NV>(a);
+}
 
 // Rows ahead for `places` 16-byte places of a thread and row, of `budget` places (12: 1024 threads of an SM can have them).
 constexpr int norm_ahead(int places, int budget = 12) {
@@ -284,7 +294,7 @@ __device__ __forceinline__ void walk_rows(uint32_t rows, char *ring, Issue issue
 // What a kernel has of shared memory: the rows ahead (PLACES 16-byte places for each thread and row), in which the column
 // sums are added at the end, or the sums themselves.
 template <typename T, int VEC, int G, int NV> struct GateFwd {
-    static constexpr Ahead A = ahead_or_none<VEC, NV>(Ahead::PAIR);
+    static constexpr Ahead A = ahead_or_none<NV>(Ahead::PAIR);
     static constexpr int PLACES = 2 * Feed<T, VEC, G, NV, A>::N, S = norm_ahead(PLACES);
     static constexpr int bytes(int threads) { return S * PLACES * 16 * threads; }
 };
@@ -292,7 +302,7 @@ template <int VEC, int G, int NV> constexpr int sums_bytes(int sums, int threads
     return sums * Sums<VEC, G, NV>::SHARED * 4 * threads + (G ? 4 * threads * NV * VEC : 0);
 }
 template <typename T, int VEC, int G, int NV> struct GateBwd {
-    static constexpr Ahead A = ahead_or_none<VEC, NV>(Ahead::RING);
+    static constexpr Ahead A = ahead_or_none<NV>(Ahead::RING);
     static constexpr int PLACES = 3 * Feed<T, VEC, G, NV, A>::N, S = norm_ahead(PLACES);
     static constexpr int bytes(int threads) {
         const int a = S * PLACES * 16 * threads, b = sums_bytes<VEC, G, NV>(1, threads);
@@ -431,12 +441,12 @@ __global__ void __launch_bounds__(MAXT, MINB) k9_gated_bwd(const __grid_constant
 
 // ---------------------------------------------------------------- before a block
 template <typename T, typename R, int VEC, int G, int NV> struct AddFwd {
-    static constexpr Ahead A = ahead_or_none<VEC, NV>(sizeof(R) == 4 ? Ahead::PAIR : Ahead::RING);
+    static constexpr Ahead A = before_block<VEC, NV>(sizeof(R) == 4 ? Ahead::PAIR : Ahead::RING);
     static constexpr int PLACES = 1 * Feed<T, VEC, G, NV, A>::N + 1 * Feed<R, VEC, G, NV, A>::N, S = norm_ahead(PLACES, 6);
     static constexpr int bytes(int threads) { return S * PLACES * 16 * threads; }
 };
 template <typename T, typename R, int VEC, int G, int NV> struct AddBwd {
-    static constexpr Ahead A = ahead_or_none<VEC, NV>(Ahead::RING);
+    static constexpr Ahead A = before_block<VEC, NV>(Ahead::RING);
     static constexpr int PLACES = 2 * Feed<T, VEC, G, NV, A>::N + 2 * Feed<R, VEC, G, NV, A>::N, S = norm_ahead(PLACES);
     static constexpr int bytes(int threads) {
         const int a = S * PLACES * 16 * threads, b = sums_bytes<VEC, G, NV>(2, threads);
