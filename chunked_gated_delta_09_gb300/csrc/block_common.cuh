@@ -77,6 +77,9 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 __device__ __forceinline__ void copy16(void *dst, const void *src, bool on) {
     asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until at most LEFT of the thread's groups of copies are under way.
 template <int LEFT> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
@@ -139,6 +142,7 @@ struct LinrecParams {
     int rows, tokens, dim, N, complement;  // rows = batch * tokens; N sequences
     int dtype, gate_dtype;
     bool vec;    // rows can be moved by tensor maps
+    bool words;  // 16-bit rows start and end on 4-byte words
     bool clear;  // the kernel clears the status word
     uint32_t spin;
     int *status;

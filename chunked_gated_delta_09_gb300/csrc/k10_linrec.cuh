@@ -307,15 +307,39 @@ template <typename T, int ROWS> struct Tile {
         const Pack<T, 2> q = *reinterpret_cast<const Pack<T, 2> *>(&v[r][ch]);
         return F2(to_f32(q.v[0]), to_f32(q.v[1]));
     }
-    // where the rows cannot be moved by a tensor map: a warp brings its own
-    __device__ __forceinline__ void bring(const void *src, int64_t ts, int tile, int wid, int cb, const LinrecParams &p) {
-        const int lane = threadIdx.x & 31, c = cb * LR_CH + lane;
-#pragma unroll 4
-        for (int r = wid * (ROWS / LR_WARPS); r < (wid + 1) * (ROWS / LR_WARPS); ++r) {
-            const int row = tile * ROWS + r;
-            T x = to_out_t<T>(0.f);
-            if (row < p.rows && c < p.dim) x = reinterpret_cast<const T *>(src)[(int64_t)row * ts + c];
-            v[r][lane] = x;
+    // Where the rows cannot be moved by a tensor map a warp brings its own: by asynchronous copies of words, or 16 single
+    // elements at a time where 16-bit rows do not start on words (32768 x 2050 bf16 with fp32 gates forward 0.214 ms, 32768
+    // x 2049 0.285; four elements at a time 0.50 and 0.52).
+    __device__ __forceinline__ void bring(const void *src_, int64_t ts, int tile, int wid, int cb, const LinrecParams &p) {
+        constexpr int N = ROWS / LR_WARPS, PER = 4 / (int)sizeof(T), LANES = LR_CH / PER;  // a word's elements, a row's words
+        const T *src = reinterpret_cast<const T *>(src_);
+        const int lane = threadIdx.x & 31, first = wid * N;
+        if (sizeof(T) == 4 || p.words) {
+            constexpr int STEP = 32 / LANES;  // rows of an access
+            const int r0 = first + lane / LANES, row0 = tile * ROWS + r0, ch = lane % LANES * PER, c = cb * LR_CH + ch;
+            const T *from = src + (int64_t)row0 * ts + c;
+            if ((tile + 1) * ROWS <= p.rows && (cb + 1) * LR_CH <= p.dim) {
+#pragma unroll
+                for (int r = 0; r < N; r += STEP, from += STEP * ts) copy4(&v[r0 + r][ch], from);
+            } else {
+                for (int r = 0; r < N; r += STEP, from += STEP * ts) {
+                    if (row0 + r < p.rows && c < p.dim) copy4(&v[r0 + r][ch], from);
+                    else *reinterpret_cast<uint32_t *>(&v[r0 + r][ch]) = 0;
+                }
+            }
+        } else {
+            const int c = cb * LR_CH + lane;
+            for (int r0 = first; r0 < first + N; r0 += 16) {
+                T x[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int row = tile * ROWS + r0 + r;
+                    x[r] = to_out_t<T>(0.f);
+                    if (row < p.rows && c < p.dim) x[r] = src[(int64_t)row * ts + c];
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) v[r0 + r][lane] = x[r];
+            }
         }
     }
 };
@@ -331,27 +355,26 @@ template <bool V> struct Const {
     static constexpr bool value = V;
 };
 
-// Four neighbouring values of a row; VEC: they lie in one aligned piece, all of them or none.
-template <bool VEC, typename T> __device__ __forceinline__ void put4(T *p, F4 v, int c, int dim) {
-    float o[4];
-    v.lo.get(o[0], o[1]), v.hi.get(o[2], o[3]);
-    if (VEC) {
-        if (c < dim) store_pack<T, 4>(p, o);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c + j < dim) p[j] = to_out_t<T>(o[j]);
-    }
-}
-template <bool VEC, typename T> __device__ __forceinline__ void put2(T *p, F2 v, int c, int dim) {
+// Four (two) neighbouring values of a row; VEC: they lie in one aligned piece, all of them or none; words: pairs of 16 bits do.
+template <bool VEC, typename T> __device__ __forceinline__ void put2(T *p, F2 v, int c, int dim, bool words) {
     float o[2];
     v.get(o[0], o[1]);
-    if (VEC) {
+    if (VEC || (sizeof(T) == 2 && words)) {
         if (c < dim) store_pack<T, 2>(p, o);
     } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (c + j < dim) p[j] = to_out_t<T>(o[j]);
+    }
+}
+template <bool VEC, typename T> __device__ __forceinline__ void put4(T *p, F4 v, int c, int dim, bool words) {
+    if (VEC) {
+        float o[4];
+        v.lo.get(o[0], o[1]), v.hi.get(o[2], o[3]);
+        if (c < dim) store_pack<T, 4>(p, o);
+    } else {
+        put2<false>(p, v.lo, c, dim, words);
+        put2<false>(p + 2, v.hi, c + 2, dim, words);
     }
 }
 __device__ __forceinline__ F2 row2(const float *p, int64_t row, int c, int dim) {
@@ -400,6 +423,12 @@ template <int ROWS, int S, int W> struct LinrecSmem {
     Ends<ROWS> ends[2];
 };
 
+// A warp's copies of its own rows have arrived, but for the LEFT groups of them issued last.
+template <int LEFT> __device__ __forceinline__ void own_rows_there() {
+    copies_wait<LEFT>();
+    __syncwarp();
+}
+
 __device__ __forceinline__ void init_barriers(uint64_t *full, int stages, Peers &peers) {
     if (threadIdx.x == 0) {
         for (int q = 0; q < stages; ++q) mbar_init(&full[q], 1);
@@ -427,7 +456,7 @@ __global__ void __launch_bounds__(LR_THREADS, 5)
     __shared__ __align__(16) LinrecSmem<ROWS, S, LR_GROUPS> sm;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = threadIdx.x >> 3, ch = 4 * (lane & 7);
     const int rank = cluster_rank(), cb = blockIdx.x / p.cluster, c = cb * LR_CH + ch;
-    const bool channels = VEC && (cb + 1) * LR_CH <= p.dim;
+    const bool channels = (cb + 1) * LR_CH <= p.dim;
 
     auto fetch = [&](int k) {  // VEC: one thread; else every warp
         const int tile = k * p.cluster + rank;
@@ -438,7 +467,7 @@ __global__ void __launch_bounds__(LR_THREADS, 5)
         } else {
             st.g[k % S].bring(p.g, p.g_ts, tile, wid, cb, p);
             st.x[k % S].bring(p.x, p.x_ts, tile, wid, cb, p);
-            __syncwarp();
+            copies_issued();
         }
     };
     init_barriers(sm.full, S, sm.peers);
@@ -464,6 +493,7 @@ __global__ void __launch_bounds__(LR_THREADS, 5)
             plain = plain && !__any_sync(0xffffffffu, heads | tails);
         }
         if (VEC) wait_phase(&sm.full[k % S], (k / S) & 1, p);
+        else own_rows_there<0>();
         F4 a[R], b[R], A, B;
         auto compose = [&](auto any) {
 #pragma unroll
@@ -489,27 +519,29 @@ __global__ void __launch_bounds__(LR_THREADS, 5)
         put_pair(&sm.maps[group][ch + 2], A.hi, B.hi);
         __syncthreads();
         // the tile's rows are in registers: their place takes the tile S further on
-        if (k + S < p.supers && (!VEC || threadIdx.x == 96)) fetch(k + S);
+        if (VEC && k + S < p.supers && threadIdx.x == 96) fetch(k + S);
         if (cuts) scan_maps<LR_GROUPS, false, true>(sm.maps, cuts, wid, lane, sm.total);
         else scan_maps<LR_GROUPS, false, false>(sm.maps, cuts, wid, lane, sm.total);
         sm.peers.tell(buf, rank, p.cluster, sm.total, cuts != 0);
         if (wid == 1) {
             wait_peers(&sm.peers.bar[buf], (k >> 1) & 1, p);
             sm.carry[lane] = sm.peers.entry(buf, rank, p.cluster, walked);
-        } else if (wid == 2) {
-            if (k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile + p.cluster, sa, sb);
+        } else {
+            if (!VEC && k + S < p.supers) fetch(k + S);  // (while the cluster's maps are on their way)
+            if (wid == 2 && k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile + p.cluster, sa, sb);
         }
         __syncthreads();
+        if (!VEC && wid == 1 && k + S < p.supers) fetch(k + S);
         const bool cut = cuts & ((1u << group) - 1);
         F4 h = {through(&sm.maps[group][ch], cut, &sm.carry[ch]), through(&sm.maps[group][ch + 2], cut, &sm.carry[ch + 2])};
         if (p.states && first % LR_SAVE == 0 && row0 < p.rows)
-            put4<VEC>(p.states + (int64_t)(row0 / LR_SAVE) * p.dim + c, h, c, p.dim);
+            put4<VEC>(p.states + (int64_t)(row0 / LR_SAVE) * p.dim + c, h, c, p.dim, false);
         T *to = reinterpret_cast<T *>(p.h) + (int64_t)row0 * p.dim + c;
         if (plain && p.h) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 h = fma4(a[r], h, b[r]);
-                put4<true>(to, h, 0, 1);
+                put4<VEC>(to, h, VEC ? 0 : c, VEC ? 1 : p.dim, p.words);
                 to += p.dim;
             }
         } else {
@@ -517,9 +549,9 @@ __global__ void __launch_bounds__(LR_THREADS, 5)
             for (int r = 0; r < R; ++r) {
                 h = (heads >> r) & 1 ? b[r] : fma4(a[r], h, b[r]);
                 if (row0 + r < p.rows) {
-                    if (p.h) put4<VEC>(to + (int64_t)r * p.dim, h, c, p.dim);
+                    if (p.h) put4<VEC>(to + (int64_t)r * p.dim, h, c, p.dim, p.words);
                     if (p.ht && (tails >> r) & 1)
-                        put4<VEC>(p.ht + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, h, c, p.dim);
+                        put4<VEC>(p.ht + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, h, c, p.dim, false);
                 }
             }
         }
@@ -546,7 +578,7 @@ __global__ void __launch_bounds__(LR_THREADS, 6)
     __shared__ __align__(16) LinrecSmem<ROWS, 4, LR_WARPS> sm;  // full: of g's two places, of those of x and dh
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, group = threadIdx.x >> 4, ch = 2 * (lane & 15);
     const int rank = cluster_rank(), cb = blockIdx.x / p.cluster, c = cb * LR_CH + ch;
-    const bool channels = VEC && (cb + 1) * LR_CH <= p.dim;
+    const bool channels = (cb + 1) * LR_CH <= p.dim;
 
     // the scan goes from the last rows to the first, in the cluster too
     auto tile_of = [&](int k) { return (p.supers - k) * p.cluster - 1 - rank; };
@@ -557,7 +589,7 @@ __global__ void __launch_bounds__(LR_THREADS, 6)
             load_tile(&st.g[buf], &maps.g, cb * LR_CH, tile * ROWS, &sm.full[buf]);
         } else {
             st.g[buf].bring(p.g, p.g_ts, tile, wid, cb, p);
-            __syncwarp();
+            copies_issued();
         }
     };
     auto fetch_x = [&](int k) {
@@ -569,7 +601,7 @@ __global__ void __launch_bounds__(LR_THREADS, 6)
         } else {
             st.x[buf].bring(p.x, p.x_ts, tile, wid, cb, p);
             st.dh[buf].bring(p.dh, p.dh_ts, tile, wid, cb, p);
-            __syncwarp();
+            copies_issued();
         }
     };
     init_barriers(sm.full, 4, sm.peers);
@@ -581,6 +613,7 @@ __global__ void __launch_bounds__(LR_THREADS, 6)
         fetch_g(0);
         fetch_x(0);
         if (p.supers > 1) fetch_g(1);
+        else if (!VEC) copies_issued();
     }
     __syncwarp();
     empty_sequences(p, rank, cb, p.dht, p.dh0);
@@ -598,11 +631,13 @@ __global__ void __launch_bounds__(LR_THREADS, 6)
         }
         const int warp0 = tile * ROWS + wid * LR_SAVE;  // the warp's first row
         // the h that enters it
-        F2 h = plain ? *reinterpret_cast<const F2 *>(p.states + (int64_t)(warp0 / LR_SAVE) * p.dim + c)
+        F2 h = VEC && plain ? *reinterpret_cast<const F2 *>(p.states + (int64_t)(warp0 / LR_SAVE) * p.dim + c)
                      : row2(warp0 < p.rows ? p.states : nullptr, warp0 / LR_SAVE, c, p.dim);
         if (VEC) {
             wait_phase(&sm.full[buf], (k >> 1) & 1, p);
             wait_phase(&sm.full[2 + buf], (k >> 1) & 1, p);
+        } else {
+            own_rows_there<1>();  // (the next tile's g may be under way)
         }
         auto dh_at = [&](int r, auto any) {  // with the gradient of the last state on a sequence's last row
             F2 d = dt.get2(first + r, ch);
@@ -645,6 +680,7 @@ __global__ void __launch_bounds__(LR_THREADS, 6)
         if (!VEC || threadIdx.x == 96) {
             if (k + 1 < p.supers) fetch_x(k + 1);
             if (k + 2 < p.supers) fetch_g(k + 2);
+            else if (!VEC) copies_issued();  // (none: what is waited for is all but the last)
         }
         if (wid == 1) {
             wait_peers(&sm.peers.bar[buf], (k >> 1) & 1, p);
@@ -672,13 +708,13 @@ __global__ void __launch_bounds__(LR_THREADS, 6)
                 const F2 d = dh_at(r, any), lam = any.value && (tails >> r) & 1 ? d : add2(d, m);
                 m = mul2(a[r], lam);
                 if (!any.value) {
-                    put2<true>(dx, COMP ? mul2(rest[r], lam) : lam, 0, 1);
-                    put2<true>(dg, mul2(m, before[r]), 0, 1);
+                    put2<VEC>(dx, COMP ? mul2(rest[r], lam) : lam, VEC ? 0 : c, VEC ? 1 : p.dim, p.words);
+                    put2<VEC>(dg, mul2(m, before[r]), VEC ? 0 : c, VEC ? 1 : p.dim, p.words);
                 } else if (row0 + r < p.rows) {
-                    put2<VEC>(dx, COMP ? mul2(rest[r], lam) : lam, c, p.dim);
-                    put2<VEC>(dg, mul2(m, before[r]), c, p.dim);
+                    put2<VEC>(dx, COMP ? mul2(rest[r], lam) : lam, c, p.dim, p.words);
+                    put2<VEC>(dg, mul2(m, before[r]), c, p.dim, p.words);
                     if (p.dh0 && (heads >> r) & 1)
-                        put2<VEC>(p.dh0 + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, m, c, p.dim);
+                        put2<VEC>(p.dh0 + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, m, c, p.dim, false);
                 }
                 dx -= p.dim, dg -= p.dim;
             }
