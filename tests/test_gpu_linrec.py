@@ -200,6 +200,29 @@ def test_blocks_of_channels(T, D):
     check(p, d, None, True)
 
 
+@pytest.mark.parametrize("dtype,gtype", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("T,D", [(3000, 100), (900, 1002), (700, 2049), (4000, 35), (129, 70)])
+def test_rows_that_are_no_multiple_of_16_bytes(T, D, dtype, gtype):
+    """Rows that start on words, and rows that do not, through many tiles and ends of sequences in them."""
+    lens = [T // 3, 1, 0, T // 2 - 1, T - T // 3 - T // 2]
+    p, d = problem(1, T, D, dtype, gtype, seed=T + D, lens=lens)
+    check(p, d, lens, True)
+
+
+@pytest.mark.parametrize("D", [64, 66])
+def test_rows_that_start_beside_a_word(D):
+    p, d = problem(1, 500, D, "bf16", "bf16", seed=D)
+    want = linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"])
+    for name, where in (("x", p), ("g", p), ("dh", d)):
+        wide = torch.zeros(1, 500, D + 2, dtype=torch.bfloat16, device="cuda")
+        wide[..., 1:-1] = where[name]
+        where[name] = wide[..., 1:-1]
+    check(p, d, None, False)
+    got = linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"])
+    for key in want:
+        assert torch.equal(want[key], got[key])
+
+
 def test_many_sequences():
     gen = torch.Generator().manual_seed(21)
     lens = torch.randint(0, 4, (2500,), generator=gen).tolist()
