@@ -143,7 +143,7 @@ struct LinrecParams {
     int dtype, gate_dtype;
     bool vec;    // rows can be moved by tensor maps
     bool words;  // 16-bit rows start and end on 4-byte words
-    bool clear;  // the kernel clears the status word
+    bool clear;  // the kernel's first CTA sets the status word
     uint32_t spin;
     int *status;
     int tiles, cluster, supers;  // tiles of rows, CTAs of a cluster, clusters' worth of rows
@@ -184,7 +184,7 @@ cudaError_t launch_gated_norm_fwd(const GatedNormParams &p, cudaStream_t stream)
 cudaError_t launch_gated_norm_bwd(const GatedNormParams &p, cudaStream_t stream);
 cudaError_t launch_add_norm_fwd(const AddNormParams &p, cudaStream_t stream);
 cudaError_t launch_add_norm_bwd(const AddNormParams &p, cudaStream_t stream);
-cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, cudaStream_t stream);
+cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, bool *narrow, cudaStream_t stream);
 cudaError_t linrec_maps(const LinrecParams &p, LinrecMaps &maps, int rows_per_tile);
 // Tensor map of rows [rows][dim] at a distance of `stride` elements, for boxes of box_rows x box_cols; what lies outside
 // reads as zero.  Base, stride and box_cols in bytes must be multiples of 16.

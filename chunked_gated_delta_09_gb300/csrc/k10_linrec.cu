@@ -43,8 +43,9 @@ cudaError_t resident(LinrecLaunch &l, Resident &out) {
 
 }  // namespace
 
-// Chooses the cluster's size and the grid for tiles of `rows_per_tile` rows x 32 channels.
-cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, cudaStream_t stream) {
+// Chooses the cluster's size and the grid for tiles of `rows_per_tile` rows x 32 channels; narrow: set instead where the
+// largest clusters would put at most two CTAs on an SM and have several tiles in turn, for which larger CTAs do better.
+cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, bool *narrow, cudaStream_t stream) {
     l.cfg = {};
     l.cfg.blockDim = dim3((unsigned)l.threads);
     l.cfg.dynamicSmemBytes = (size_t)l.smem;
@@ -59,6 +60,10 @@ cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, cud
     p.tiles = p.rows > 0 ? (p.rows + rows_per_tile - 1) / rows_per_tile : 1;
     p.per_seq = FastDiv::of((uint32_t)(p.tokens > 0 ? p.tokens : 1));
     const int64_t nblk = (p.dim + LR_CH - 1) / LR_CH;
+    if (narrow && p.tiles > LR_MAX_CLUSTER && 5 * LR_MAX_CLUSTER * nblk <= 2 * r.clusters[1]) {
+        *narrow = true;
+        return cudaSuccess;
+    }
     // The size whose clusters take the fewest tiles one after the other, all waves of them together.  A tile takes about 2 %
     // longer with each CTA more, from the exchange of the maps (48763 x 4096 bf16, backward: 6 CTAs, 127 tiles in turn,
     // 0.404 ms; 5 CTAs, 153 tiles, 0.426 ms; 10 CTAs in two waves, 154 tiles, 0.432 ms; 7 CTAs in two, 218, 0.497 ms); a wave
@@ -74,8 +79,9 @@ cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, cud
     p.supers = (p.tiles + p.cluster - 1) / p.cluster;
     l.cfg.gridDim = dim3((unsigned)(nblk * p.cluster));
     l.attr.val.clusterDim.x = (unsigned)p.cluster;
-    // malformed cu_seqlens, or waits that a short limit makes expire, may be noted before any CTA could clear the word
-    p.clear = !p.cu && p.spin >= (1u << 16);
+    // One CTA checks short lists in about the time of the other's first tile and sets the status word, which saves the launch that
+    // clears it.  (Waits that a short limit makes expire may be noted before that.)
+    p.clear = (!p.cu || p.N <= 1024) && p.spin >= (1u << 16);
     return p.clear ? cudaSuccess : cudaMemsetAsync(p.status, 0, sizeof(int), stream);
 }
 
