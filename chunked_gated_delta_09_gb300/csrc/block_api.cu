@@ -21,18 +21,26 @@ bool type_ok(int d) { return d == GDR_F32 || d == GDR_BF16 || d == GDR_F16; }
 int64_t type_size(int d) { return d == GDR_F32 ? 4 : 2; }
 bool at(const void *p, int64_t a) { return (uintptr_t)p % (uintptr_t)a == 0; }
 
-// Collects whether every tensor of a call can be moved in pieces of `n` elements (16 bytes at most at a time), or in words
-// of 4 bytes.
+// Collects whether every tensor of a call can be moved in pieces of `n` elements (16 bytes at most at a time).
 struct VecRule {
     int64_t n;
-    bool ok = true, words = true, natural = true;
+    bool ok = true, natural = true;
     explicit VecRule(int64_t n_) : n(n_) {}
     void tensor(const void *p, int dtype, int64_t stride0 = 0, int64_t stride1 = 0) {
         if (!p) return;
         const int64_t s = type_size(dtype), need = n * s < 16 ? n * s : 16;
         natural = natural && at(p, s);
         ok = ok && at(p, need) && stride0 * s % need == 0 && stride1 * s % need == 0;
-        words = words && at(p, 4) && stride0 * s % 4 == 0 && stride1 * s % 4 == 0;
+    }
+};
+
+// The largest pieces of rows of `dim` elements, 4, 2 or 1 of them, that start at multiples of their size in every tensor.
+struct Pieces {
+    int n;
+    explicit Pieces(int64_t dim) : n(dim % 4 == 0 ? 4 : dim % 2 == 0 ? 2 : 1) {}
+    void tensor(const void *p, int dtype, int64_t stride) {
+        const int64_t s = type_size(dtype);
+        while (n > 1 && !(at(p, n * s) && stride % n == 0)) n /= 2;
     }
 };
 
@@ -267,7 +275,10 @@ gdr_status gdr_linrec_fwd(const gdr_linrec_fwd_args *a, void *stream_) {
     p.N = (int)(a->num_seqs > 0 ? a->num_seqs : a->batch), p.complement = a->complement;
     p.dtype = a->dtype, p.gate_dtype = a->gate_dtype;
     p.vec = v.ok && rows > 0 && map_rows(a->x_token_stride, rows, a->dim) && map_rows(a->g_token_stride, rows, a->dim);
-    p.words = v.words;
+    Pieces x(a->dim), g(a->dim);
+    x.tensor(a->x, a->dtype, a->x_token_stride), x.tensor(a->h, a->dtype, a->dim);
+    g.tensor(a->g, a->gate_dtype, a->g_token_stride);
+    p.x_piece = x.n, p.g_piece = g.n;
     p.status = (int *)a->workspace, p.spin = spin_limit();
     return done(launch_linrec_fwd(p, stream));
 }
@@ -307,7 +318,11 @@ gdr_status gdr_linrec_bwd(const gdr_linrec_bwd_args *a, void *stream_) {
     p.dtype = a->dtype, p.gate_dtype = a->gate_dtype;
     p.vec = v.ok && rows > 0 && map_rows(a->x_token_stride, rows, a->dim) && map_rows(a->g_token_stride, rows, a->dim) &&
             map_rows(a->dh_token_stride, rows, a->dim);
-    p.words = v.words;
+    Pieces x(a->dim), g(a->dim);
+    x.tensor(a->x, a->dtype, a->x_token_stride), x.tensor(a->dh, a->dtype, a->dh_token_stride);
+    x.tensor(a->dx, a->dtype, a->dim);
+    g.tensor(a->g, a->gate_dtype, a->g_token_stride), g.tensor(a->dg, a->gate_dtype, a->dim);
+    p.x_piece = x.n, p.g_piece = g.n;
     p.status = (int *)a->workspace, p.spin = spin_limit();
     return done(launch_linrec_bwd(p, stream));
 }

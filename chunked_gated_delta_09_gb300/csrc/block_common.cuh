@@ -77,8 +77,8 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 __device__ __forceinline__ void copy16(void *dst, const void *src, bool on) {
     asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copy4(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+template <int BYTES> __device__ __forceinline__ void copy_piece(void *dst, const void *src) {  // 4, 8 or 16
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until at most LEFT of the thread's groups of copies are under way.
@@ -142,7 +142,7 @@ struct LinrecParams {
     int rows, tokens, dim, N, complement;  // rows = batch * tokens; N sequences
     int dtype, gate_dtype;
     bool vec;    // rows can be moved by tensor maps
-    bool words;  // 16-bit rows start and end on 4-byte words
+    int x_piece, g_piece;  // else: elements moved together in rows of activations and of gates, 4, 2 or 1
     bool clear;  // the kernel's first CTA sets the status word
     uint32_t spin;
     int *status;

@@ -307,39 +307,50 @@ template <typename T, int ROWS> struct Tile {
         const Pack<T, 2> q = *reinterpret_cast<const Pack<T, 2> *>(&v[r][ch]);
         return F2(to_f32(q.v[0]), to_f32(q.v[1]));
     }
-    // Where the rows cannot be moved by a tensor map a warp brings its own: by asynchronous copies of words, or 16 single
-    // elements at a time where 16-bit rows do not start on words (32768 x 2050 bf16 with fp32 gates forward 0.214 ms, 32768
-    // x 2049 0.285; four elements at a time 0.50 and 0.52).  N: rows of a warp.
-    template <int N> __device__ __forceinline__ void bring(const void *src_, int64_t ts, int tile, int wid, int cb, const LinrecParams &p) {
-        constexpr int PER = 4 / (int)sizeof(T), LANES = LR_CH / PER;  // a word's elements, a row's words
-        const T *src = reinterpret_cast<const T *>(src_);
-        const int lane = threadIdx.x & 31, first = wid * N;
-        if (sizeof(T) == 4 || p.words) {
-            constexpr int STEP = 32 / LANES;  // rows of an access
-            const int r0 = first + lane / LANES, row0 = tile * ROWS + r0, ch = lane % LANES * PER, c = cb * LR_CH + ch;
-            const T *from = src + (int64_t)row0 * ts + c;
-            if ((tile + 1) * ROWS <= p.rows && (cb + 1) * LR_CH <= p.dim) {
+    // Where the rows cannot be moved by a tensor map a warp brings its own N: by asynchronous copies of pieces, or 16 single
+    // elements at a time where those have 16 bits and nothing larger is aligned (32768 x 2052 bf16 with fp32 gates forward
+    // 0.189 ms, 2050 0.196, 2049 0.264; by registers, 16 loads at a time, 0.265, 0.297 and 0.323).
+    template <int N>
+    __device__ __forceinline__ void bring(const void *src, int64_t ts, int piece, int tile, int wid, int cb, const LinrecParams &p) {
+        const T *from = reinterpret_cast<const T *>(src);
+        if (piece == 4) pieces<N, 4>(from, ts, tile, wid, cb, p);
+        else if (piece == 2) pieces<N, 2>(from, ts, tile, wid, cb, p);
+        else if constexpr (sizeof(T) == 4) pieces<N, 1>(from, ts, tile, wid, cb, p);
+        else singles<N>(from, ts, tile, wid, cb, p);
+    }
+    template <int N, int E>
+    __device__ __forceinline__ void pieces(const T *src, int64_t ts, int tile, int wid, int cb, const LinrecParams &p) {
+        constexpr int LANES = LR_CH / E, STEP = 32 / LANES, BYTES = E * (int)sizeof(T);
+        const int lane = threadIdx.x & 31, r0 = wid * N + lane / LANES, row0 = tile * ROWS + r0, ch = lane % LANES * E;
+        const int c = cb * LR_CH + ch;
+        const T *from = src + (int64_t)row0 * ts + c;
+        if ((tile + 1) * ROWS <= p.rows && (cb + 1) * LR_CH <= p.dim) {
 #pragma unroll
-                for (int r = 0; r < N; r += STEP, from += STEP * ts) copy4(&v[r0 + r][ch], from);
-            } else {
-                for (int r = 0; r < N; r += STEP, from += STEP * ts) {
-                    if (row0 + r < p.rows && c < p.dim) copy4(&v[r0 + r][ch], from);
-                    else *reinterpret_cast<uint32_t *>(&v[r0 + r][ch]) = 0;
-                }
-            }
+            for (int r = 0; r < N; r += STEP, from += STEP * ts) copy_piece<BYTES>(&v[r0 + r][ch], from);
         } else {
-            const int c = cb * LR_CH + lane;
-            for (int r0 = first; r0 < first + N; r0 += 16) {
-                T x[16];
+            for (int r = 0; r < N; r += STEP, from += STEP * ts) {
+                if (row0 + r < p.rows && c < p.dim) {
+                    copy_piece<BYTES>(&v[r0 + r][ch], from);
+                } else {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int row = tile * ROWS + r0 + r;
-                    x[r] = to_out_t<T>(0.f);
-                    if (row < p.rows && c < p.dim) x[r] = src[(int64_t)row * ts + c];
+                    for (int j = 0; j < E; ++j) v[r0 + r][ch + j] = to_out_t<T>(0.f);
                 }
-#pragma unroll
-                for (int r = 0; r < 16; ++r) v[r0 + r][lane] = x[r];
             }
+        }
+    }
+    template <int N>
+    __device__ __forceinline__ void singles(const T *src, int64_t ts, int tile, int wid, int cb, const LinrecParams &p) {
+        const int lane = threadIdx.x & 31, c = cb * LR_CH + lane;
+        for (int r0 = wid * N; r0 < (wid + 1) * N; r0 += 16) {
+            T x[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = tile * ROWS + r0 + r;
+                x[r] = to_out_t<T>(0.f);
+                if (row < p.rows && c < p.dim) x[r] = src[(int64_t)row * ts + c];
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) v[r0 + r][lane] = x[r];
         }
     }
 };
@@ -355,11 +366,11 @@ template <bool V> struct Const {
     static constexpr bool value = V;
 };
 
-// Four (two) neighbouring values of a row; VEC: they lie in one aligned piece, all of them or none; words: pairs of 16 bits do.
-template <bool VEC, typename T> __device__ __forceinline__ void put2(T *p, F2 v, int c, int dim, bool words) {
+// Two or four neighbouring values of a row, of which `piece` at a time are aligned and lie inside together; VEC: all.
+template <bool VEC, typename T> __device__ __forceinline__ void put2(T *p, F2 v, int c, int dim, int piece) {
     float o[2];
     v.get(o[0], o[1]);
-    if (VEC || (sizeof(T) == 2 && words)) {
+    if (VEC || piece >= 2) {
         if (c < dim) store_pack<T, 2>(p, o);
     } else {
 #pragma unroll
@@ -367,14 +378,14 @@ template <bool VEC, typename T> __device__ __forceinline__ void put2(T *p, F2 v,
             if (c + j < dim) p[j] = to_out_t<T>(o[j]);
     }
 }
-template <bool VEC, typename T> __device__ __forceinline__ void put4(T *p, F4 v, int c, int dim, bool words) {
-    if (VEC) {
+template <bool VEC, typename T> __device__ __forceinline__ void put4(T *p, F4 v, int c, int dim, int piece) {
+    if (VEC || piece == 4) {
         float o[4];
         v.lo.get(o[0], o[1]), v.hi.get(o[2], o[3]);
         if (c < dim) store_pack<T, 4>(p, o);
     } else {
-        put2<false>(p, v.lo, c, dim, words);
-        put2<false>(p + 2, v.hi, c + 2, dim, words);
+        put2<false>(p, v.lo, c, dim, piece);
+        put2<false>(p + 2, v.hi, c + 2, dim, piece);
     }
 }
 __device__ __forceinline__ F2 row2(const float *p, int64_t row, int c, int dim) {
@@ -475,8 +486,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : 2)
             load_tile(&st.g[k % S], &maps.g, cb * LR_CH, tile * ROWS, &sm.full[k % S]);
             load_tile(&st.x[k % S], &maps.x, cb * LR_CH, tile * ROWS, &sm.full[k % S]);
         } else {
-            st.g[k % S].template bring<LR_FWD_PER * R>(p.g, p.g_ts, tile, wid, cb, p);
-            st.x[k % S].template bring<LR_FWD_PER * R>(p.x, p.x_ts, tile, wid, cb, p);
+            st.g[k % S].template bring<LR_FWD_PER * R>(p.g, p.g_ts, p.g_piece, tile, wid, cb, p);
+            st.x[k % S].template bring<LR_FWD_PER * R>(p.x, p.x_ts, p.x_piece, tile, wid, cb, p);
             copies_issued();
         }
     };
@@ -529,29 +540,27 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : 2)
         put_pair(&sm.maps[group][ch + 2], A.hi, B.hi);
         __syncthreads();
         // the tile's rows are in registers: their place takes the tile S further on
-        if (VEC && k + S < p.supers && threadIdx.x == 96) fetch(k + S);
+        if (k + S < p.supers && (!VEC || threadIdx.x == 96)) fetch(k + S);
         if (cuts) scan_maps<WARPS, GROUPS, false, true>(sm.maps, cuts, wid, lane, sm.total);
         else scan_maps<WARPS, GROUPS, false, false>(sm.maps, cuts, wid, lane, sm.total);
         sm.peers.template tell<WARPS>(buf, rank, p.cluster, sm.total, cuts != 0);
         if (wid == 1) {
             wait_peers(&sm.peers.bar[buf], (k >> 1) & 1, p);
             sm.carry[lane] = sm.peers.entry(buf, rank, p.cluster, walked);
-        } else {
-            if (!VEC && k + S < p.supers) fetch(k + S);  // (while the cluster's maps are on their way)
-            if (wid == 2 && k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile + p.cluster, sa, sb);
+        } else if (wid == 2) {
+            if (k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile + p.cluster, sa, sb);
         }
         __syncthreads();
-        if (!VEC && wid == 1 && k + S < p.supers) fetch(k + S);
         const bool cut = cuts & ((1u << group) - 1);
         F4 h = {through(&sm.maps[group][ch], cut, &sm.carry[ch]), through(&sm.maps[group][ch + 2], cut, &sm.carry[ch + 2])};
         if (p.states && first % LR_SAVE == 0 && row0 < p.rows)
-            put4<VEC>(p.states + (int64_t)(row0 / LR_SAVE) * p.dim + c, h, c, p.dim, false);
+            put4<VEC>(p.states + (int64_t)(row0 / LR_SAVE) * p.dim + c, h, c, p.dim, 1);
         T *to = reinterpret_cast<T *>(p.h) + (int64_t)row0 * p.dim + c;
         if (plain && p.h) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 h = fma4(a[r], h, b[r]);
-                put4<VEC>(to, h, VEC ? 0 : c, VEC ? 1 : p.dim, p.words);
+                put4<VEC>(to, h, VEC ? 0 : c, VEC ? 1 : p.dim, p.x_piece);
                 to += p.dim;
             }
         } else {
@@ -559,9 +568,9 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : 2)
             for (int r = 0; r < R; ++r) {
                 h = (heads >> r) & 1 ? b[r] : fma4(a[r], h, b[r]);
                 if (row0 + r < p.rows) {
-                    if (p.h) put4<VEC>(to + (int64_t)r * p.dim, h, c, p.dim, p.words);
+                    if (p.h) put4<VEC>(to + (int64_t)r * p.dim, h, c, p.dim, p.x_piece);
                     if (p.ht && (tails >> r) & 1)
-                        put4<VEC>(p.ht + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, h, c, p.dim, false);
+                        put4<VEC>(p.ht + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, h, c, p.dim, 1);
                 }
             }
         }
@@ -598,7 +607,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 6 : 3)
             mbar_expect_tx(&sm.full[buf], sizeof(st.g[0]));
             load_tile(&st.g[buf], &maps.g, cb * LR_CH, tile * ROWS, &sm.full[buf]);
         } else {
-            st.g[buf].template bring<LR_BWD_PER * R>(p.g, p.g_ts, tile, wid, cb, p);
+            st.g[buf].template bring<LR_BWD_PER * R>(p.g, p.g_ts, p.g_piece, tile, wid, cb, p);
             copies_issued();
         }
     };
@@ -609,8 +618,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 6 : 3)
             load_tile(&st.x[buf], &maps.x, cb * LR_CH, tile * ROWS, &sm.full[2 + buf]);
             load_tile(&st.dh[buf], &maps.dh, cb * LR_CH, tile * ROWS, &sm.full[2 + buf]);
         } else {
-            st.x[buf].template bring<LR_BWD_PER * R>(p.x, p.x_ts, tile, wid, cb, p);
-            st.dh[buf].template bring<LR_BWD_PER * R>(p.dh, p.dh_ts, tile, wid, cb, p);
+            st.x[buf].template bring<LR_BWD_PER * R>(p.x, p.x_ts, p.x_piece, tile, wid, cb, p);
+            st.dh[buf].template bring<LR_BWD_PER * R>(p.dh, p.dh_ts, p.x_piece, tile, wid, cb, p);
             copies_issued();
         }
     };
@@ -718,13 +727,13 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 6 : 3)
                 const F2 d = dh_at(r, any), lam = any.value && (tails >> r) & 1 ? d : add2(d, m);
                 m = mul2(a[r], lam);
                 if (!any.value) {
-                    put2<VEC>(dx, COMP ? mul2(rest[r], lam) : lam, VEC ? 0 : c, VEC ? 1 : p.dim, p.words);
-                    put2<VEC>(dg, mul2(m, before[r]), VEC ? 0 : c, VEC ? 1 : p.dim, p.words);
+                    put2<VEC>(dx, COMP ? mul2(rest[r], lam) : lam, VEC ? 0 : c, VEC ? 1 : p.dim, p.x_piece);
+                    put2<VEC>(dg, mul2(m, before[r]), VEC ? 0 : c, VEC ? 1 : p.dim, p.g_piece);
                 } else if (row0 + r < p.rows) {
-                    put2<VEC>(dx, COMP ? mul2(rest[r], lam) : lam, c, p.dim, p.words);
-                    put2<VEC>(dg, mul2(m, before[r]), c, p.dim, p.words);
+                    put2<VEC>(dx, COMP ? mul2(rest[r], lam) : lam, c, p.dim, p.x_piece);
+                    put2<VEC>(dg, mul2(m, before[r]), c, p.dim, p.g_piece);
                     if (p.dh0 && (heads >> r) & 1)
-                        put2<VEC>(p.dh0 + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, m, c, p.dim, false);
+                        put2<VEC>(p.dh0 + (int64_t)ends.sequence_of(p, row0 + r) * p.dim + c, m, c, p.dim, 1);
                 }
                 dx -= p.dim, dg -= p.dim;
             }

@@ -223,6 +223,20 @@ def test_rows_that_start_beside_a_word(D):
         assert torch.equal(want[key], got[key])
 
 
+@pytest.mark.parametrize("dtype,T,D", [("bf16", 40, 35), ("bf16", 700, 66), ("f32", 40, 37), ("f16", 300, 35)])
+def test_rows_whose_stride_is_wider_than_they_are(dtype, T, D):
+    """The columns between the rows hold nans, of which nothing is read."""
+    p, d = problem(1, T, D, dtype, dtype, seed=T + D)
+    for name, where in (("x", p), ("g", p), ("dh", d)):
+        wide = torch.full((T * 72,), float("nan"), dtype=TYPES[dtype], device="cuda")
+        view = torch.as_strided(wide, (1, T, D), (T * 72, 72, 1))
+        view.copy_(where[name])
+        where[name] = view
+    check(p, d, None, True)
+    got = linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], complement=True)
+    assert all(torch.isfinite(v.float()).all() for v in got.values())
+
+
 def test_many_sequences():
     gen = torch.Generator().manual_seed(21)
     lens = torch.randint(0, 4, (2500,), generator=gen).tolist()
