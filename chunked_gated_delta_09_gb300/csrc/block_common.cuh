@@ -177,8 +177,25 @@ struct StepParams {
 // CTAs that write partial column sums, at most (the workspace is sized for it).
 constexpr int NORM_MAX_PARTS = 152 * 8;
 int norm_parts(int64_t rows, int64_t dim);
-cudaError_t norm_grid(const void *kernel, int threads, int smem, int max_smem, int64_t rows, int rows_per_cta,
+cudaError_t norm_grid(const void *kernel, int threads, int ctas, int smem, int max_smem, int64_t rows, int rows_per_cta,
                       int most, int &grid);
+// A launch whose CTAs form clusters of `ctas`.
+struct ClusterLaunch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = {};
+    ClusterLaunch(int grid, int threads, int smem, int ctas, cudaStream_t stream) {
+        cfg.gridDim = dim3((unsigned)grid);
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = (size_t)smem;
+        cfg.stream = stream;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)ctas;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+    }
+    ClusterLaunch(const ClusterLaunch &) = delete;
+};
 
 cudaError_t launch_gated_norm_fwd(const GatedNormParams &p, cudaStream_t stream);
 cudaError_t launch_gated_norm_bwd(const GatedNormParams &p, cudaStream_t stream);

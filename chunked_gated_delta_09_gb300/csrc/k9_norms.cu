@@ -1,6 +1,7 @@
 // k9_norms.cu -- the norms around a block: choice by type, and the sum of the partial column sums (dweight, dscale).
+#include <map>
 #include <mutex>
-#include <unordered_map>
+#include <tuple>
 
 #include "block_common.cuh"
 
@@ -8,27 +9,35 @@ namespace gdr {
 
 namespace {
 std::mutex g_mu;
-std::unordered_map<const void *, int> g_resident[64][33];  // per device and number of warps: CTAs that it holds
+// per device, by kernel, warps of a CTA and CTAs of a cluster: CTAs (clusters) that it holds
+std::map<std::tuple<const void *, int, int>, int> g_resident[64];
 }  // namespace
 
-// CTAs of a persistent grid: as many as the device holds at a time, no more than there are rows for, and at most `most`.
+// CTAs of a persistent grid, or its clusters of `ctas`: as many as the device holds at a time, no more than there are rows for,
+// and at most `most`.
 // max_smem: with the most threads that the kernel is launched with.
-cudaError_t norm_grid(const void *kernel, int threads, int smem, int max_smem, int64_t rows, int rows_per_cta, int most, int &grid) {
+cudaError_t norm_grid(const void *kernel, int threads, int ctas, int smem, int max_smem, int64_t rows, int rows_per_cta, int most,
+                      int &grid) {
     int dev = 0, n = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     {
         std::lock_guard<std::mutex> lock(g_mu);
         int fresh = 0;
-        int &held = dev >= 0 && dev < 64 ? g_resident[dev][threads / 32][kernel] : fresh;
+        int &held = dev >= 0 && dev < 64 ? g_resident[dev][{kernel, threads / 32, ctas}] : fresh;
         if (!held) {
             int sms = 0, per_sm = 0;
             if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem)) != cudaSuccess)
                 return e;
-            if ((e = device_sm_count(&sms)) != cudaSuccess) return e;
-            if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem)) != cudaSuccess) return e;
-            if (per_sm < 1) return cudaErrorInvalidConfiguration;
-            held = sms * per_sm;
+            if (ctas > 1) {
+                ClusterLaunch l(ctas, threads, smem, ctas, nullptr);
+                if ((e = cudaOccupancyMaxActiveClusters(&held, kernel, &l.cfg)) != cudaSuccess) return e;
+            } else {
+                if ((e = device_sm_count(&sms)) != cudaSuccess) return e;
+                if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem)) != cudaSuccess) return e;
+                held = sms * per_sm;
+            }
+            if (held < 1) return cudaErrorInvalidConfiguration;
         }
         n = held;
     }

@@ -10,10 +10,13 @@
 // 6.8 TB/s.  After a block, 32768 x 16 x 128 bf16: forward 0.064 ms (6.3 TB/s), backward 0.126 ms with its column sums (5.3
 // TB/s; instructions are issued in 79 % of the cycles, the activation and its derivative for every element).  Before one:
 // forward 48763 x 4096 bf16 0.252 ms (6.3), backward 0.309 (6.5); 32768 x 2048 bf16 on an fp32 stream 0.134 (6.0), backward
-// with the gradient of the scale 0.198 (6.1).  Few rows take the time of a launch.  A row belongs to 8, 16 or 32 lanes or to
-// a whole CTA, a thread holding one piece of VEC elements where the row fits 1024 threads.  Lanes sum by shuffles, CTAs
-// through shared memory.  The grid is persistent: the weights are read once per thread, and the column sums
-// of a backward (dw, ds) stay in registers until the CTA writes its partial row, which k9_colsum adds in a fixed order.
+// with the gradient of the scale 0.198 (6.1).  Few rows take the time of a launch.  A row belongs to 8, 16 or 32 lanes, to
+// a whole CTA of up to 1024 threads, a piece of VEC elements for each, or to a cluster of CTAs of up to 512 (4000 x 16384 bf16
+// on an fp32 stream forward 0.159 ms, backward 0.242; one CTA with two pieces to a thread 0.177, 0.368; clusters of CTAs of
+// 1024, one to an SM, 0.179, 0.257; for 8000 x 8192 one CTA is faster, 0.129, 0.216 against 0.151, 0.225).  Lanes sum by
+// shuffles, CTAs and clusters through shared memory.  The grid is persistent: the weights are read once per thread, and the
+// column sums of a backward (dw, ds) stay in registers until the CTA writes its partial row, which k9_colsum adds in a fixed
+// order.
 // The rows ahead come in one of three ways (see Ahead), whichever measured fastest for the kernel.
 #pragma once
 
@@ -36,24 +39,59 @@ template <typename T> __device__ __forceinline__ float sigmoid_t(float z) {
 }
 constexpr int ACT_NONE = 2;  // besides the C interface's silu and sigmoid
 
-// Sums of two values over the row's threads (G lanes, or the whole CTA for G = 0), in the same order whatever the row.
+// A row's threads: G lanes, a whole CTA, or the CTAs of a cluster.
+constexpr int WHOLE = 0, SPREAD = -1, MAX_SPREAD = 8;
+
+__device__ __forceinline__ int cluster_rank() {
+    int r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ int cluster_ctas() {
+    int n;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ void cluster_meet() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Sums of two values over the row's threads, in the same order whatever the row.
 template <int G> struct GroupSum {
-    float2 *red;  // [2][warps] in shared memory (G = 0)
+    static constexpr int PLACES = G > 0 ? 1 : 2 * 32 * (G == SPREAD ? MAX_SPREAD : 1);
+    float2 *red;  // [2][CTAs][32 warps] in shared memory
     int buf = 0;
-    __device__ __forceinline__ explicit GroupSum(float2 *r) : red(r) {}
+    __device__ __forceinline__ explicit GroupSum(float2 *r) : red(r) {
+        if (G == SPREAD) cluster_meet();  // every CTA runs: its shared memory may be written
+    }
     // TWO: b is wanted too
     template <bool TWO = true> __device__ __forceinline__ float2 operator()(float a, float b) {
 #pragma unroll
-        for (int o = (G ? G : 32) / 2; o > 0; o >>= 1) {
+        for (int o = (G > 0 ? G : 32) / 2; o > 0; o >>= 1) {
             a += __shfl_xor_sync(0xffffffffu, a, o);
             if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
         }
-        if constexpr (G == 0) {
+        if constexpr (G <= 0) {
             // two buffers in turn: a warp can only be back at this one after the next row's barrier
-            const int nw = blockDim.x / 32, lane = threadIdx.x & 31;
-            if (lane == 0) red[buf * 32 + (threadIdx.x >> 5)] = make_float2(a, b);
-            __syncthreads();
-            const float2 x = lane < nw ? red[buf * 32 + lane] : make_float2(0.f, 0.f);
+            const int nw = blockDim.x / 32, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+            float2 x = make_float2(0.f, 0.f);
+            if constexpr (G == SPREAD) {
+                const int ctas = cluster_ctas();
+                float2 *at = red + buf * MAX_SPREAD * 32;
+                if (lane < ctas) {  // a lane for each CTA, its own among them
+                    uint32_t to;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(at + cluster_rank() * 32 + w)), "r"(lane));
+                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(a), "f"(b) : "memory");
+                }
+                cluster_meet();
+                for (int q = 0; q < ctas; ++q)
+                    if (lane < nw) x.x += at[q * 32 + lane].x, x.y += at[q * 32 + lane].y;
+            } else {
+                if (lane == 0) red[buf * 32 + w] = make_float2(a, b);
+                __syncthreads();
+                if (lane < nw) x = red[buf * 32 + lane];
+            }
             a = x.x, b = x.y;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
@@ -79,15 +117,20 @@ struct NormGrad {
 template <int VEC, int G, int NV> struct Cols {
     int t, step, dim;
     bool on[NV];
-    __device__ __forceinline__ explicit Cols(int dim_) : t(G ? threadIdx.x % (G ? G : 1) : threadIdx.x), step(G ? G : blockDim.x), dim(dim_) {
+    __device__ __forceinline__ explicit Cols(int dim_)
+        : t(G > 0 ? threadIdx.x % (G > 0 ? G : 1) : threadIdx.x + (G == SPREAD ? cluster_rank() * blockDim.x : 0)),
+          step(G > 0 ? G : blockDim.x), dim(dim_) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) on[i] = (t + i * step) * VEC < dim;
     }
     __device__ __forceinline__ int at(int i) const { return (t + i * step) * VEC; }
 };
 // Rows that a CTA works on at a time, and the thread's among them.
-template <int G> __device__ __forceinline__ int cta_rows() { return G ? NORM_THREADS / (G ? G : 1) : 1; }
-template <int G> __device__ __forceinline__ int cta_row() { return G ? threadIdx.x / (G ? G : 1) : 0; }
+template <int G> __device__ __forceinline__ int cta_rows() { return G > 0 ? NORM_THREADS / (G > 0 ? G : 1) : 1; }
+template <int G> __device__ __forceinline__ int cta_row() { return G > 0 ? threadIdx.x / (G > 0 ? G : 1) : 0; }
+// What shares out the rows, CTAs or clusters, and which of them this is.
+template <int G> __device__ __forceinline__ uint32_t walkers() { return G == SPREAD ? gridDim.x / cluster_ctas() : gridDim.x; }
+template <int G> __device__ __forceinline__ uint32_t walker() { return G == SPREAD ? blockIdx.x / cluster_ctas() : blockIdx.x; }
 
 // How the rows ahead come.
 //   RING   by asynchronous copies to places in shared memory, several rows ahead, which takes no registers: the backward
@@ -96,9 +139,9 @@ template <int G> __device__ __forceinline__ int cta_row() { return G ? threadIdx
 //   PAIR   the next row's pieces in registers while a row is worked on: the forward after a block (32768 x 16 x 128 bf16
 //          0.064 ms; RING 0.072), before one on an fp32 stream (32768 x 2048 0.134; RING 0.141), and before one by single
 //          elements, up to 4 to a thread (20000 x 1001 fp32 stream, backward 0.088 ms; NONE 0.135)
-//   NONE   a row's pieces when it is its turn, other CTAs covering the wait: rows of several pieces to a thread, for which
-//          there are no registers (4000 x 16384 fp32 stream, backward 0.368 ms; PAIR 0.712), and after a block single
-//          elements too (20000 x 1001 forward 0.049 ms, backward 0.089; PAIR 0.063, 0.094)
+//   NONE   a row's pieces when it is its turn, other CTAs covering the wait: more than 4 single elements to a thread, for
+//          which there are no registers, and after a block any number (20000 x 1001 forward 0.049 ms, backward 0.089; PAIR
+//          0.063, 0.094)
 enum class Ahead { NONE, PAIR, RING };
 
 // How a thread gets its pieces of a row of one tensor; zeros where there is nothing.  In a RING a piece of two 16-byte places
@@ -107,7 +150,7 @@ enum class Ahead { NONE, PAIR, RING };
 template <typename T, int VEC, int G, int NV, Ahead A> struct Feed {
     static constexpr bool LATE = A == Ahead::NONE && NV * VEC > 8;  // read where it is used: registers would not hold it
     static constexpr int N = A == Ahead::RING ? VEC * (int)sizeof(T) / 16 : 0;  // 16-byte places of a thread
-    static constexpr int L = G ? G : 32;                                        // lanes that copy for each other
+    static constexpr int L = G > 0 ? G : 32;                                    // lanes that copy for each other
     Pack<T, VEC> v[A == Ahead::RING || LATE ? 1 : NV];
     const T *row;
     const Cols<VEC, G, NV> *cols;
@@ -206,23 +249,23 @@ __device__ __forceinline__ void store_piece(void *p, int64_t at, const Cols<VEC,
     if (live && c.on[i]) store_pack<T, VEC>(reinterpret_cast<T *>(p) + at + c.at(i), x);
 }
 
-// Where a CTA's column sums go: its partial row, or the result itself where it is the only CTA.
-struct ColumnSums {
+// Where a CTA's column sums go: its (or its cluster's) partial row, or the result itself where it is the only one.
+template <int G> struct ColumnSums {
     float *part;
     void *out;
     int dtype;
     __device__ __forceinline__ ColumnSums(float *p, void *o, int dt, int which, int dim)
-        : part(p + ((size_t)which * gridDim.x + blockIdx.x) * dim), out(o), dtype(dt) {}
+        : part(p + ((size_t)which * walkers<G>() + walker<G>()) * dim), out(o), dtype(dt) {}
     __device__ __forceinline__ void put(int col, float x) const {
-        if (gridDim.x == 1) store_scalar(out, col, x, dtype);
+        if (walkers<G>() == 1) store_scalar(out, col, x, dtype);
         else part[col] = x;
     }
 };
 // The rows' threads are added in order, in `smem` that nothing else uses by then.
 template <int VEC, int G, int NV>
-__device__ __forceinline__ void write_sums(const ColumnSums &to, float *smem, const Cols<VEC, G, NV> &c, int dim,
+__device__ __forceinline__ void write_sums(const ColumnSums<G> &to, float *smem, const Cols<VEC, G, NV> &c, int dim,
                                            Sums<VEC, G, NV> &acc) {
-    if constexpr (G == 0) {
+    if constexpr (G <= 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (c.on[i])
@@ -248,9 +291,9 @@ __device__ __forceinline__ void write_sums(const ColumnSums &to, float *smem, co
 // The rows of a persistent CTA.  In: a row's feeds; issue(in, place, row, live), work(in, place, row, live).
 template <class In, Ahead A, int G, int S, int PLACES, class Issue, class Work>
 __device__ __forceinline__ void walk_rows(uint32_t rows, char *ring, Issue issue, Work work) {
-    const uint32_t step = gridDim.x * cta_rows<G>();
+    const uint32_t step = walkers<G>() * cta_rows<G>();
     // (whole warps stay together: a row's lanes may lie beyond the last row)
-    uint32_t base = blockIdx.x * cta_rows<G>(), row = base + cta_row<G>();
+    uint32_t base = walker<G>() * cta_rows<G>(), row = base + cta_row<G>();
     if constexpr (A == Ahead::RING) {
         In in;
         const uint32_t bytes = PLACES * 16 * blockDim.x;
@@ -299,7 +342,7 @@ template <typename T, int VEC, int G, int NV> struct GateFwd {
     static constexpr int bytes(int threads) { return S * PLACES * 16 * threads; }
 };
 template <int VEC, int G, int NV> constexpr int sums_bytes(int sums, int threads) {
-    return sums * Sums<VEC, G, NV>::SHARED * 4 * threads + (G ? 4 * threads * NV * VEC : 0);
+    return sums * Sums<VEC, G, NV>::SHARED * 4 * threads + (G > 0 ? 4 * threads * NV * VEC : 0);
 }
 template <typename T, int VEC, int G, int NV> struct GateBwd {
     static constexpr Ahead A = ahead_or_none<NV>(Ahead::RING);
@@ -316,7 +359,7 @@ __device__ __forceinline__ void gated_fwd(const GatedNormParams &p, char *ring) 
     struct In {
         Feed<T, VEC, G, NV, L::A> x, z;
     };
-    __shared__ float2 red[G ? 1 : 64];
+    __shared__ float2 red[GroupSum<G>::PLACES];
     GroupSum<G> sum(red);
     const Cols<VEC, G, NV> c(p.dim);
     const Weights<VEC, G, NV> weight(p.weight, p.weight_dtype, c, 1.f);
@@ -365,7 +408,7 @@ __device__ __forceinline__ void gated_bwd(const GatedNormParams &p, char *ring, 
     struct In {
         Feed<T, VEC, G, NV, L::A> x, dy, z;
     };
-    __shared__ float2 red[G ? 1 : 64];
+    __shared__ float2 red[GroupSum<G>::PLACES];
     GroupSum<G> sum(red);
     const Cols<VEC, G, NV> c(p.dim);
     const Weights<VEC, G, NV> weight(p.weight, p.weight_dtype, c, 1.f);
@@ -463,7 +506,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k9_add_fwd(const __grid_constant__
         Feed<R, VEC, G, NV, L::A> r;
     };
     extern __shared__ __align__(16) char norm_smem[];
-    __shared__ float2 red[G ? 1 : 64];
+    __shared__ float2 red[GroupSum<G>::PLACES];
     GroupSum<G> sum(red);
     const Cols<VEC, G, NV> c(p.dim);
     const Weights<VEC, G, NV> weight(p.weight, p.weight_dtype, c, 1.f), scale(p.scale_vec, p.scale_dtype, c, p.scale);
@@ -515,7 +558,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k9_add_bwd(const __grid_constant__
     };
     extern __shared__ __align__(16) char norm_smem[];
     float *shared = reinterpret_cast<float *>(norm_smem);
-    __shared__ float2 red[G ? 1 : 64];
+    __shared__ float2 red[GroupSum<G>::PLACES];
     GroupSum<G> sum(red);
     const Cols<VEC, G, NV> c(p.dim);
     const Weights<VEC, G, NV> weight(p.weight, p.weight_dtype, c, 1.f), scale(p.scale_vec, p.scale_dtype, c, p.scale);
@@ -574,28 +617,33 @@ __global__ void __launch_bounds__(MAXT, MINB) k9_add_bwd(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- choice of the row's threads
-// CALL(VEC, G, NV, most threads, threads): one piece to a thread up to 1024 threads, in whole warps.
+// CALL(VEC, G, NV, most threads, threads) with `ctas` CTAs to a row: one piece to a thread up to 8 x 512 threads, in whole
+// warps; single elements, several to a thread.
 #define NORM_DISPATCH(T, vec, dim, CALL)                                                      \
     do {                                                                                      \
+        int ctas = 1;                                                                         \
         if (vec) {                                                                            \
             constexpr int VE = 16 / (int)sizeof(T);                                           \
             const int n = (dim) / VE, up = (n + 31) / 32 * 32;                                \
             if (n <= 8) { CALL(VE, 8, 1, NORM_THREADS, NORM_THREADS); }                       \
             else if (n <= 16) { CALL(VE, 16, 1, NORM_THREADS, NORM_THREADS); }                \
             else if (n <= 32) { CALL(VE, 32, 1, NORM_THREADS, NORM_THREADS); }                \
-            else if (n <= 256) { CALL(VE, 0, 1, 256, up); }                                   \
-            else if (n <= 512) { CALL(VE, 0, 1, 512, up); }                                   \
-            else if (n <= 1024) { CALL(VE, 0, 1, 1024, up); }                                 \
-            else if (n <= 2048) { CALL(VE, 0, 2, 1024, 1024); }                               \
-            else { CALL(VE, 0, VE == 4 ? 4 : 2, 1024, 1024); }                                \
+            else if (n <= 256) { CALL(VE, WHOLE, 1, 256, up); }                               \
+            else if (n <= 512) { CALL(VE, WHOLE, 1, 512, up); }                               \
+            else if (n <= 1024) { CALL(VE, WHOLE, 1, 1024, up); }                             \
+            else {                                                                            \
+                ctas = (n + 511) / 512;                                                       \
+                const int per = ((n + ctas - 1) / ctas + 31) / 32 * 32;                       \
+                CALL(VE, SPREAD, 1, 512, per);                                                \
+            }                                                                                 \
         } else {                                                                              \
             const int up = ((dim) + 63) / 64 * 32;                                            \
             if ((dim) <= 128) { CALL(1, 32, 4, NORM_THREADS, NORM_THREADS); }                 \
-            else if ((dim) <= 512) { CALL(1, 0, 2, 256, up); }                                \
-            else if ((dim) <= 1024) { CALL(1, 0, 2, 512, up); }                               \
-            else if ((dim) <= 2048) { CALL(1, 0, 2, 1024, up); }                              \
-            else if ((dim) <= 4096) { CALL(1, 0, 4, 1024, 1024); }                            \
-            else { CALL(1, 0, 16, 1024, 1024); }                                              \
+            else if ((dim) <= 512) { CALL(1, WHOLE, 2, 256, up); }                                \
+            else if ((dim) <= 1024) { CALL(1, WHOLE, 2, 512, up); }                               \
+            else if ((dim) <= 2048) { CALL(1, WHOLE, 2, 1024, up); }                              \
+            else if ((dim) <= 4096) { CALL(1, WHOLE, 4, 1024, 1024); }                            \
+            else { CALL(1, WHOLE, 16, 1024, 1024); }                                              \
         }                                                                                     \
     } while (0)
 
@@ -603,15 +651,21 @@ __global__ void __launch_bounds__(MAXT, MINB) k9_add_bwd(const __grid_constant__
 // 1 us, a second launch 2 us on the device and 8 us on the host where the device waits for it.
 inline int sum_ctas(int64_t rows, int rows_per_cta, int dim) { return rows <= 4 * rows_per_cta ? 1 : norm_parts(rows, dim); }
 
-// Launches the persistent grid of a kernel; L says what shared memory it takes; grid: its number of CTAs, at most `most`.
-template <class L, class K, class P>
-cudaError_t norm_launch(K kernel, const P &p, int threads, int max_threads, int rows_per_cta, int most, int &grid,
-                        cudaStream_t stream) {
+// Launches the persistent grid of a kernel; L says what shared memory it takes; grid: its number of CTAs (of clusters where
+// several CTAs share a row), at most `most`.
+template <class L, class P>
+cudaError_t norm_launch(void (*kernel)(P), const P &p, int threads, int max_threads, int ctas, int rows_per_cta, int most,
+                        int &grid, cudaStream_t stream) {
     const int smem = L::bytes(threads);
-    cudaError_t e = norm_grid((const void *)kernel, threads, smem, L::bytes(max_threads), p.rows, rows_per_cta, most, grid);
+    cudaError_t e =
+        norm_grid((const void *)kernel, threads, ctas, smem, L::bytes(max_threads), p.rows, rows_per_cta, most, grid);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, threads, smem, stream>>>(p);
-    return cudaGetLastError();
+    if (ctas == 1) {
+        kernel<<<grid, threads, smem, stream>>>(p);
+        return cudaGetLastError();
+    }
+    ClusterLaunch l(grid * ctas, threads, smem, ctas, stream);
+    return cudaLaunchKernelEx(&l.cfg, kernel, p);
 }
 
 }  // namespace
@@ -621,16 +675,18 @@ cudaError_t launch_colsum(const float *part, int parts, int dim, int sums, void 
 
 // CTAs of an SM that a kernel is compiled for, of `threads` threads at most: 1024 threads in all; 2048 for the forward before a
 // block, which needs few registers (48763 x 4096 bf16 0.276 -> 0.258 ms); 512 for the backward before a block with longer
-// rows, whose column sums take them.
-constexpr int add_fwd_ctas(int residual_size, int vec, int pieces, int threads) {
-    return (residual_size == 4 || vec == 1 || pieces > 1 ? 1024 : 2048) / threads;
+// rows in one CTA, whose column sums take them.
+constexpr int add_fwd_ctas(int residual_size, int vec, int threads) {
+    return (residual_size == 4 || vec == 1 ? 1024 : 2048) / threads;
 }
-constexpr int add_bwd_ctas(int vec, int threads) { return threads <= 256 || vec == 1 ? 1024 / threads : 1; }
-#define NORM_ROWS(G) ((G) ? NORM_THREADS / ((G) ? (G) : 1) : 1)
+constexpr int add_bwd_ctas(int vec, int g, int threads) {
+    return threads <= 256 || vec == 1 || g == SPREAD ? 1024 / threads : 1;
+}
+#define NORM_ROWS(G) ((G) > 0 ? NORM_THREADS / ((G) > 0 ? (G) : 1) : 1)
 template <typename T> cudaError_t gated_norm_fwd_t(const GatedNormParams &p, cudaStream_t stream) {
     int grid = 0;
 #define CALL(V, G, NV, MAXT, threads)                                                                                  \
-    return norm_launch<GateFwd<T, V, G, NV>>(k9_gated_fwd<T, V, G, NV, MAXT, 1024 / MAXT>, p, threads, MAXT, NORM_ROWS(G), \
+    return norm_launch<GateFwd<T, V, G, NV>>(k9_gated_fwd<T, V, G, NV, MAXT, 1024 / MAXT>, p, threads, MAXT, ctas, NORM_ROWS(G), \
                     1 << 30, grid, stream)
     NORM_DISPATCH(T, p.vec, p.dim, CALL);
 #undef CALL
@@ -640,7 +696,7 @@ template <typename T> cudaError_t gated_norm_bwd_t(const GatedNormParams &p, cud
     int grid = 0;
     cudaError_t e = cudaSuccess;
 #define CALL(V, G, NV, MAXT, threads)                                                                                  \
-    e = norm_launch<GateBwd<T, V, G, NV>>(k9_gated_bwd<T, V, G, NV, MAXT, 1024 / MAXT>, p, threads, MAXT, NORM_ROWS(G), \
+    e = norm_launch<GateBwd<T, V, G, NV>>(k9_gated_bwd<T, V, G, NV, MAXT, 1024 / MAXT>, p, threads, MAXT, ctas, NORM_ROWS(G), \
                     sum_ctas(p.rows, NORM_ROWS(G), p.dim), grid, stream)
     NORM_DISPATCH(T, p.vec, p.dim, CALL);
 #undef CALL
@@ -651,7 +707,7 @@ template <typename T> cudaError_t gated_norm_bwd_t(const GatedNormParams &p, cud
 template <typename T, typename R> cudaError_t add_norm_fwd_t(const AddNormParams &p, cudaStream_t stream) {
     int grid = 0;
 #define CALL(V, G, NV, MAXT, threads)                                                                                  \
-    return norm_launch<AddFwd<T, R, V, G, NV>>(k9_add_fwd<T, R, V, G, NV, MAXT, add_fwd_ctas(sizeof(R), V, NV, MAXT)>, p, threads, MAXT, NORM_ROWS(G), \
+    return norm_launch<AddFwd<T, R, V, G, NV>>(k9_add_fwd<T, R, V, G, NV, MAXT, add_fwd_ctas(sizeof(R), V, MAXT)>, p, threads, MAXT, ctas, NORM_ROWS(G), \
                     1 << 30, grid, stream)
     NORM_DISPATCH(T, p.vec, p.dim, CALL);
 #undef CALL
@@ -661,7 +717,7 @@ template <typename T, typename R> cudaError_t add_norm_bwd_t(const AddNormParams
     int grid = 0;
     cudaError_t e = cudaSuccess;
 #define CALL(V, G, NV, MAXT, threads)                                                                                  \
-    e = norm_launch<AddBwd<T, R, V, G, NV>>(k9_add_bwd<T, R, V, G, NV, MAXT, add_bwd_ctas(V, MAXT)>, p, threads, MAXT, NORM_ROWS(G), \
+    e = norm_launch<AddBwd<T, R, V, G, NV>>(k9_add_bwd<T, R, V, G, NV, MAXT, add_bwd_ctas(V, G, MAXT)>, p, threads, MAXT, ctas, NORM_ROWS(G), \
                     sum_ctas(p.rows, NORM_ROWS(G), p.dim), grid, stream)
     NORM_DISPATCH(T, p.vec, p.dim, CALL);
 #undef CALL

@@ -120,6 +120,19 @@ def test_add_norm_many_rows():
     check_gated(x, z, 1.0 + U.randn(gen, 48, times=0.2), dy, "silu")
 
 
+@pytest.mark.parametrize("dtype,rtype", [("f32", "f32"), ("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("dim", [4104, 8200, 12288, 16376])
+def test_rows_that_several_ctas_share(dim, dtype, rtype):
+    """More rows than the device holds clusters, whose last CTAs have fewer columns."""
+    gen = U.seeded(dim)
+    dt, rt = TYPES[dtype], TYPES[rtype]
+    x, dy = (U.randn(gen, 331, dim, dtype=dt) for _ in range(2))
+    res, dres = (U.randn(gen, 331, dim, dtype=rt, times=2.0) for _ in range(2))
+    w, s = (1.0 + U.randn(gen, dim, times=0.2) for _ in range(2))
+    check_add(x, res, w, s, dy, dres)
+    check_gated(x.view(331, 1, dim), res.to(dt).view(331, 1, dim), w, dy.view(331, 1, dim), "silu")
+
+
 def test_add_norm_parts_may_be_absent():
     gen = U.seeded(13)
     x, dy = (U.randn(gen, 2, 11, 80, dtype=torch.bfloat16) for _ in range(2))
