@@ -21,11 +21,13 @@ bool type_ok(int d) { return d == GDR_F32 || d == GDR_BF16 || d == GDR_F16; }
 int64_t type_size(int d) { return d == GDR_F32 ? 4 : 2; }
 bool at(const void *p, int64_t a) { return (uintptr_t)p % (uintptr_t)a == 0; }
 
-// Collects whether every tensor of a call can be moved in pieces of `n` elements (16 bytes at most at a time).
+// Collects whether every tensor of a call can be moved in pieces of `n` elements (16 bytes at most at a time).  The width is
+// part of the rule by itself: a thread has whole pieces, also in a call whose outputs, of stride `dim`, are all absent.
 struct VecRule {
     int64_t n;
-    bool ok = true, natural = true;
-    explicit VecRule(int64_t n_) : n(n_) {}
+    bool ok, natural = true;
+    VecRule(int64_t n_, int64_t dim) : VecRule(n_, dim, n_) {}
+    VecRule(int64_t n_, int64_t dim, int64_t whole) : n(n_), ok(dim % whole == 0) {}  // whole: elements that a thread stores together
     void tensor(const void *p, int dtype, int64_t stride0 = 0, int64_t stride1 = 0) {
         if (!p) return;
         const int64_t s = type_size(dtype), need = n * s < 16 ? n * s : 16;
@@ -82,7 +84,7 @@ gdr_status gdr_gated_norm_fwd(const gdr_gated_norm_fwd_args *a, void *stream) {
     if (!a->x || !a->y) return GDR_ERR_INVALID_ARG;
     if (a->x_token_stride < 0 || a->x_head_stride < 0 || a->z_token_stride < 0 || a->z_head_stride < 0)
         return GDR_ERR_INVALID_ARG;
-    VecRule v(16 / type_size(a->dtype));
+    VecRule v(16 / type_size(a->dtype), a->dim);
     v.tensor(a->x, a->dtype, a->x_token_stride, a->x_head_stride);
     v.tensor(a->z, a->dtype, a->z_token_stride, a->z_head_stride);
     v.tensor(a->y, a->dtype, a->dim);
@@ -118,7 +120,7 @@ gdr_status gdr_gated_norm_bwd(const gdr_gated_norm_bwd_args *a, void *stream_) {
     if (a->x_token_stride < 0 || a->x_head_stride < 0 || a->z_token_stride < 0 || a->z_head_stride < 0 ||
         a->dy_token_stride < 0 || a->dy_head_stride < 0)
         return GDR_ERR_INVALID_ARG;
-    VecRule v(16 / type_size(a->dtype));
+    VecRule v(16 / type_size(a->dtype), a->dim);
     v.tensor(a->dy, a->dtype, a->dy_token_stride, a->dy_head_stride);
     v.tensor(a->x, a->dtype, a->x_token_stride, a->x_head_stride);
     v.tensor(a->z, a->dtype, a->z_token_stride, a->z_head_stride);
@@ -153,7 +155,7 @@ gdr_status gdr_add_norm_fwd(const gdr_add_norm_fwd_args *a, void *stream) {
     if (a->x_token_stride < 0 || a->residual_token_stride < 0 ||
         (a->residual_out && !(a->tokens <= 1 || a->residual_out_token_stride >= a->dim)))
         return GDR_ERR_INVALID_ARG;
-    VecRule v(16 / type_size(a->dtype));
+    VecRule v(16 / type_size(a->dtype), a->dim);
     v.tensor(a->x, a->dtype, a->x_token_stride);
     v.tensor(a->residual, a->residual_dtype, a->residual_token_stride);
     v.tensor(a->residual_out, a->residual_dtype, a->residual_out_token_stride);
@@ -196,7 +198,7 @@ gdr_status gdr_add_norm_bwd(const gdr_add_norm_bwd_args *a, void *stream_) {
         return GDR_ERR_INVALID_ARG;
     if (a->dy_token_stride < 0 || a->dres_token_stride < 0 || a->residual_out_token_stride < 0 || a->x_token_stride < 0)
         return GDR_ERR_INVALID_ARG;
-    VecRule v(16 / type_size(a->dtype));
+    VecRule v(16 / type_size(a->dtype), a->dim);
     v.tensor(a->dy, a->dtype, a->dy_token_stride);
     v.tensor(a->dres, a->residual_dtype, a->dres_token_stride);
     v.tensor(a->residual_out, a->residual_dtype, a->residual_out_token_stride);
@@ -259,7 +261,7 @@ gdr_status gdr_linrec_fwd(const gdr_linrec_fwd_args *a, void *stream_) {
     if (!a->workspace || !at(a->workspace, 256) || a->workspace_bytes < gdr_linrec_workspace_bytes(rows, a->dim))
         return GDR_ERR_INVALID_ARG;
     if (!at(a->h0, 4) || !at(a->ht, 4) || !at(a->states, 4) || !at(a->cu_seqlens, 4)) return GDR_ERR_INVALID_ARG;
-    VecRule v(8);  // tensor maps take multiples of 16 bytes
+    VecRule v(8, a->dim, 4);  // tensor maps take multiples of 16 bytes, lanes have 4 channels at most
     v.tensor(a->x, a->dtype, a->x_token_stride);
     v.tensor(a->g, a->gate_dtype, a->g_token_stride);
     v.tensor(a->h, a->dtype, a->dim);
@@ -297,7 +299,7 @@ gdr_status gdr_linrec_bwd(const gdr_linrec_bwd_args *a, void *stream_) {
         return GDR_ERR_INVALID_ARG;
     if (!at(a->h0, 4) || !at(a->dht, 4) || !at(a->states, 4) || !at(a->dh0, 4) || !at(a->cu_seqlens, 4))
         return GDR_ERR_INVALID_ARG;
-    VecRule v(8);  // tensor maps take multiples of 16 bytes
+    VecRule v(8, a->dim, 4);  // tensor maps take multiples of 16 bytes, lanes have 4 channels at most
     v.tensor(a->x, a->dtype, a->x_token_stride);
     v.tensor(a->g, a->gate_dtype, a->g_token_stride);
     v.tensor(a->dh, a->dtype, a->dh_token_stride);
@@ -349,7 +351,7 @@ gdr_status gdr_linrec_step(const gdr_linrec_step_args *a, void *stream) {
     if (!a->x || !a->g || !a->y || (a->num_slots > 0 && !a->state)) return GDR_ERR_INVALID_ARG;
     if (a->x_token_stride < 0 || a->g_token_stride < 0 || !at(a->slots, 4) || !at(a->state, 4))
         return GDR_ERR_INVALID_ARG;
-    VecRule v(4);
+    VecRule v(4, a->dim);
     v.tensor(a->x, a->dtype, a->x_token_stride);
     v.tensor(a->g, a->gate_dtype, a->g_token_stride);
     v.tensor(a->y, a->dtype, a->dim);
