@@ -331,10 +331,12 @@ gdr_status gdr_linrec_bwd(const gdr_linrec_bwd_args *a, void *stream_) {
 
 gdr_status gdr_linrec_get_status(void *workspace, void *stream_) {
     if (!workspace || !at(workspace, 256)) return GDR_ERR_INVALID_ARG;
+    cudaStream_t stream = (cudaStream_t)stream_;
     int word = 0;
-    if (cudaStreamSynchronize((cudaStream_t)stream_) != cudaSuccess) return GDR_ERR_CUDA;
-    if (cudaMemcpy(&word, workspace, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return GDR_ERR_CUDA;
-    if (cudaMemset(workspace, 0, sizeof(int)) != cudaSuccess) return GDR_ERR_CUDA;
+    // all of it on the caller's stream, and done on return: the workspace may be given away then
+    if (cudaMemcpyAsync(&word, workspace, sizeof(int), cudaMemcpyDeviceToHost, stream) != cudaSuccess) return GDR_ERR_CUDA;
+    if (cudaMemsetAsync(workspace, 0, sizeof(int), stream) != cudaSuccess) return GDR_ERR_CUDA;
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return GDR_ERR_CUDA;
     if (word & ST_TIMEOUT) return GDR_ERR_TIMEOUT;
     return word & ST_BAD_SEQLENS ? GDR_ERR_DEVICE : GDR_OK;
 }

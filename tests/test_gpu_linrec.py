@@ -304,3 +304,21 @@ def test_capture_in_a_graph_and_other_streams():
     out = linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"], stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+def test_the_status_is_read_on_the_calls_own_stream():
+    """Work on the default stream is not waited for, and nothing is left to be done to the workspace on return."""
+    p, _ = problem(1, 500, 64, "bf16", "f32", seed=30)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ref = linrec_fwd(p["x"], p["g"], p["h0"], stream=side, check_status=True)  # (loads and allocates what the call needs)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(1_000_000_000)
+    busy = torch.cuda.Event()
+    busy.record()
+    out = linrec_fwd(p["x"], p["g"], p["h0"], stream=side, check_status=True)
+    with torch.cuda.stream(side):
+        again = torch.full((256,), 255, dtype=torch.uint8, device="cuda")  # the workspace's block, as a rule
+    assert not busy.query()
+    torch.cuda.synchronize()
+    assert (again == 255).all() and all(torch.equal(a, b) for a, b in zip(ref, out))
