@@ -317,8 +317,8 @@ def test_the_status_is_read_on_the_calls_own_stream():
     busy = torch.cuda.Event()
     busy.record()
     out = linrec_fwd(p["x"], p["g"], p["h0"], stream=side, check_status=True)
+    assert not busy.query()
     with torch.cuda.stream(side):
         again = torch.full((256,), 255, dtype=torch.uint8, device="cuda")  # the workspace's block, as a rule
-    assert not busy.query()
     torch.cuda.synchronize()
     assert (again == 255).all() and all(torch.equal(a, b) for a, b in zip(ref, out))
