@@ -554,9 +554,10 @@ gdr_status gdr_bwd_get_status(gdr_bwd_plan *plan, void *workspace, void *stream_
     cudaStream_t stream = (cudaStream_t)stream_;
     int word = 0;
     int *dev = reinterpret_cast<int *>(reinterpret_cast<char *>(workspace) + plan->o_status);
+    // all of it on the caller's stream, and done on return: the workspace may be given away then
+    if (cudaMemcpyAsync(&word, dev, sizeof(int), cudaMemcpyDeviceToHost, stream) != cudaSuccess) return GDR_ERR_CUDA;
+    if (cudaMemsetAsync(dev, 0, sizeof(int), stream) != cudaSuccess) return GDR_ERR_CUDA;
     if (cudaStreamSynchronize(stream) != cudaSuccess) return GDR_ERR_CUDA;
-    if (cudaMemcpy(&word, dev, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return GDR_ERR_CUDA;
-    if (cudaMemset(dev, 0, sizeof(int)) != cudaSuccess) return GDR_ERR_CUDA;
     if (word & ST_TIMEOUT) return GDR_ERR_TIMEOUT;
     if (word & (ST_BAD_SEQLENS | ST_RANGE)) return GDR_ERR_DEVICE;
     return GDR_OK;

@@ -57,3 +57,26 @@ def test_inputs_beyond_fp16_range_report_device_error(dtype):
     # the same problem within range is accepted
     ok = make_problem("range_ok", B=1, T=200, Hk=1, Hv=2, K=64, V=64, qkv_dtype=dtype, seed=8)
     assert _run_status(ok, ops.plan_for(ok)) == _lib.GDR_OK
+
+
+def test_the_status_is_read_on_the_calls_own_stream():
+    """Work on the default stream is not waited for, and nothing is left to be done to the workspace on return."""
+    prob = make_problem("side", B=1, T=256, Hk=1, Hv=2, K=64, V=64, seed=21)
+    plan, dev = ops.plan_for(prob), ops.problem_to_device(prob, "cuda")
+    out, ws = plan.alloc_outputs("cuda"), plan.alloc_workspace("cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plan.run(out=out, workspace=ws, stream=side, **dev)  # (loads what the call needs)
+    assert plan.get_status(ws, side) == _lib.GDR_OK
+    torch.cuda.synchronize()
+    torch.cuda._sleep(1_000_000_000)
+    busy = torch.cuda.Event()
+    busy.record()
+    plan.run(out=out, workspace=ws, stream=side, **dev)
+    assert plan.get_status(ws, side) == _lib.GDR_OK
+    assert not busy.query()
+    with torch.cuda.stream(side):
+        ws.fill_(255)
+    torch.cuda.synchronize()
+    assert (ws == 255).all()
+    compare(prob, {k: v.double().cpu().numpy() for k, v in out.items()}, oracle.problem_backward(prob))
