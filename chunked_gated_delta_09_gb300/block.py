@@ -366,12 +366,14 @@ def _linrec_check(x, g, h0, cu_seqlens):
     return index, B, T, D, N
 
 
-def _linrec_done(ws, check_status, index):
+def _linrec_done(workspaces, check_status, index):
+    """Waits for a call's passes, of which each has its own workspace (an address), and raises what they reported."""
     if check_status:
         with torch.cuda.device(index):
-            st = _entry("gdr_linrec_get_status")(ws.data_ptr(), _raw_stream(index))
-        if st:
-            raise GdrError(st, "gdr_linrec_get_status")
+            for ws in workspaces:
+                st = _entry("gdr_linrec_get_status")(ws, _raw_stream(index))
+                if st:
+                    raise GdrError(st, "gdr_linrec_get_status")
 
 
 def linrec_fwd(x, g, h0=None, cu_seqlens=None, *, complement=False, return_states=False, stream=None,
@@ -399,7 +401,7 @@ def linrec_fwd(x, g, h0=None, cu_seqlens=None, *, complement=False, return_state
            _pack_linrec_fwd(x.data_ptr(), g.data_ptr(), _ptr(h0), _ptr(cu_seqlens), h.data_ptr(), ht.data_ptr(),
                             _ptr(states), ws.data_ptr(), B, T, D, 0 if cu_seqlens is None else N, _token_stride(x, "x"),
                             _token_stride(g, "g"), nbytes, _DT[x.dtype], _DT[g.dtype], int(complement), 0), index)
-    _linrec_done(ws, check_status, index)
+    _linrec_done([ws.data_ptr()], check_status, index)
     return (h, ht, states) if return_states else (h, ht)
 
 
@@ -419,15 +421,18 @@ def linrec_bwd(x, g, dh, h0=None, dht=None, cu_seqlens=None, states=None, *, com
         _need(dht.is_contiguous(), "dht must be contiguous")
     dev = x.device
     nbytes = _entry("gdr_linrec_workspace_bytes")(B * T, D)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    # (a pass starts by clearing its workspace's status: two passes in one would lose the first one's)
+    ws = torch.empty(nbytes if states is not None else 2 * nbytes, dtype=torch.uint8, device=dev)
+    passes = [ws.data_ptr()]
     tiles = -(-B * T // _lib.LINREC_SAVE)
     strides = _token_stride(x, "x"), _token_stride(g, "g")
     seqs = 0 if cu_seqlens is None else N
     if states is None:
         states = torch.empty(tiles, D, dtype=_F32, device=dev)
+        passes.append(passes[0] + nbytes)
         _queue("gdr_linrec_fwd",
                _pack_linrec_fwd(x.data_ptr(), g.data_ptr(), _ptr(h0), _ptr(cu_seqlens), 0, 0, states.data_ptr(),
-                                ws.data_ptr(), B, T, D, seqs, *strides, nbytes, _DT[x.dtype], _DT[g.dtype],
+                                passes[1], B, T, D, seqs, *strides, nbytes, _DT[x.dtype], _DT[g.dtype],
                                 int(complement), 0), index)
     else:
         _like(states, "states", index, (tiles, D), _F32)
@@ -437,10 +442,10 @@ def linrec_bwd(x, g, dh, h0=None, dht=None, cu_seqlens=None, states=None, *, com
     dh0 = torch.empty(N, D, dtype=_F32, device=dev)
     _queue("gdr_linrec_bwd",
            _pack_linrec_bwd(x.data_ptr(), g.data_ptr(), dh.data_ptr(), _ptr(h0), _ptr(dht), states.data_ptr(),
-                            _ptr(cu_seqlens), dx.data_ptr(), dg.data_ptr(), dh0.data_ptr(), ws.data_ptr(), B, T, D, seqs,
+                            _ptr(cu_seqlens), dx.data_ptr(), dg.data_ptr(), dh0.data_ptr(), passes[0], B, T, D, seqs,
                             *strides, _token_stride(dh, "dh"), nbytes, _DT[x.dtype], _DT[g.dtype], int(complement), 0),
            index)
-    _linrec_done(ws, check_status, index)
+    _linrec_done(passes, check_status, index)
     return dict(dx=dx, dg=dg, dh0=dh0)
 
 

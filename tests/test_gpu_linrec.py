@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import block_util as U
-from chunked_gated_delta_09_gb300 import GdrError, _lib, linear_recurrence, linrec_bwd, linrec_fwd, linrec_step
+from chunked_gated_delta_09_gb300 import GdrError, _lib, block, linear_recurrence, linrec_bwd, linrec_fwd, linrec_step
 
 pytestmark = pytest.mark.gpu
 
@@ -322,3 +322,51 @@ def test_the_status_is_read_on_the_calls_own_stream():
         again = torch.full((256,), 255, dtype=torch.uint8, device="cuda")  # the workspace's block, as a rule
     torch.cuda.synchronize()
     assert (again == 255).all() and all(torch.equal(a, b) for a, b in zip(ref, out))
+
+
+@pytest.mark.parametrize("short", ["gdr_linrec_fwd", "gdr_linrec_bwd"])
+def test_waits_that_run_out_in_either_pass_of_a_backward_are_reported(short, monkeypatch):
+    """A backward without saved states runs the forward first; a limit of one poll for one of the two passes alone."""
+    p, d = problem(1, 6000, 256, "bf16", "f32", seed=31)
+    _, _, states = linrec_fwd(p["x"], p["g"], p["h0"], return_states=True)
+    ref = linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], states=states, check_status=True)
+    queue = block._queue
+
+    def limited(name, packed, index):
+        with monkeypatch.context() as m:
+            if name == short:
+                m.setenv("GDR_SPIN_LIMIT", "1")
+            queue(name, packed, index)
+
+    with monkeypatch.context() as m:
+        m.setattr(block, "_queue", limited)
+        for kept in (None, states):
+            statuses = []
+            for _ in range(3):
+                try:
+                    linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], states=kept, check_status=True)
+                    statuses.append(_lib.GDR_OK)
+                except GdrError as e:
+                    statuses.append(e.status)
+            expected = short == "gdr_linrec_bwd" or kept is None
+            assert (_lib.GDR_ERR_TIMEOUT in statuses) == expected, statuses
+            assert set(statuses) <= {_lib.GDR_OK, _lib.GDR_ERR_TIMEOUT}, statuses
+    again = linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], check_status=True)
+    assert all(torch.equal(ref[k], again[k]) for k in ref)
+
+
+def test_malformed_lists_of_many_sequences_are_reported():
+    """More sequences than one CTA checks; no lengths but the list is out of order, or ends early."""
+    lens = [3] * 2000
+    p, d = problem(1, 6000, 40, "f32", "f32", seed=32, lens=lens)
+    _, _, states = linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"], return_states=True, check_status=True)
+    for at, value in ((1999, 5000), (700, 6001), (0, 1), (2000, 5999)):
+        bad = p["cu_seqlens"].clone()
+        bad[at] = value
+        for call in (lambda: linrec_fwd(p["x"], p["g"], p["h0"], bad, check_status=True),
+                     lambda: linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], bad, states, check_status=True),
+                     lambda: linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], bad, check_status=True)):
+            with pytest.raises(GdrError) as e:
+                call()
+            assert e.value.status == _lib.GDR_ERR_DEVICE
+    linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"], check_status=True)
