@@ -443,7 +443,8 @@ __device__ __forceinline__ void gated_bwd(const GatedNormParams &p, char *ring, 
                 }
             }
             const float2 s = sum(s1, s2);
-            const float rs = rsqrtf(s.x * inv_dim + p.eps);
+            // (a row past the end is zeros and adds nothing to the column sums, also where eps is 0)
+            const float rs = G <= 0 || live ? rsqrtf(s.x * inv_dim + p.eps) : 0.f;
             const NormGrad q(rs, s.y * inv_dim, p.dim, p.eps);
             const int64_t o = (int64_t)row * p.dim;
 #pragma unroll
@@ -455,7 +456,7 @@ __device__ __forceinline__ void gated_bwd(const GatedNormParams &p, char *ring, 
                     const float xr = x[i][j] * rs;
                     dx[j] = q(up[i][j] * w[j], x[i][j]);
                     if (ACT != ACT_NONE) dz[i][j] *= xr * w[j];
-                    dw.at(i, j) = fmaf(up[i][j], xr, dw.at(i, j));  // (rows past the end hold zeros)
+                    dw.at(i, j) = fmaf(up[i][j], xr, dw.at(i, j));
                 }
                 store_piece<T>(p.dx, o, c, i, live, dx);
                 if (ACT != ACT_NONE) store_piece<T>(p.dz, o, c, i, live, dz[i]);
@@ -588,7 +589,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k9_add_bwd(const __grid_constant__
                 }
             }
             const float2 s = sum(s1, s2);
-            const float rs = rsqrtf(s.x * inv_dim + p.eps);
+            // (a row past the end is zeros and adds nothing to the column sums, also where eps is 0)
+            const float rs = G <= 0 || live ? rsqrtf(s.x * inv_dim + p.eps) : 0.f;
             const NormGrad q(rs, s.y * inv_dim, p.dim, p.eps);
             const int64_t o = (int64_t)row * p.dim;
 #pragma unroll

@@ -251,3 +251,21 @@ def test_capture_in_a_graph():
         got = gated_norm_bwd(dy, x, z, w)
     graph.replay()
     assert all(torch.equal(got[k], ref[k]) for k in ref)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 3, 37, 300])
+@pytest.mark.parametrize("dim", [5, 64, 100, 128, 200, 256, 700])
+def test_eps_of_zero(dim, rows, dtype):
+    """No row here is zero, so nothing divides by zero: rows past the end, of which a CTA has some, must not either."""
+    dt, gen = TYPES[dtype], U.seeded(dim + rows)
+    x, z, dy = (U.randn(gen, rows, 1, dim, dtype=dt) for _ in range(3))
+    w, s = (1.0 + U.randn(gen, dim, times=0.2) for _ in range(2))
+    got = dict(y=gated_norm_fwd(x, z, w, eps=0.0))
+    got.update(gated_norm_bwd(dy, x, z, w, eps=0.0))
+    U.check(got, U.gated_norm(x, z, w, 0.0, "silu", dy))
+    x, res, dy, dres = x[:, 0], z[:, 0].float(), dy[:, 0], U.randn(gen, rows, dim)
+    y, r = add_norm_fwd(x, res, w, s, eps=0.0)
+    U.check(dict(y=y, r=r), U.add_norm_fwd(x, res, w, s, 0.0))
+    got = add_norm_bwd(dy, dres, r, w, s, x=x, eps=0.0)
+    U.check(got, U.add_norm_bwd(dy, dres, r, w, s, x, 0.0))
