@@ -7,7 +7,7 @@
 
 As in :mod:`ops`, everything is computed by libgdrbwd.so's kernels: this module checks tensors, allocates outputs and
 workspace with torch and passes raw pointers.  ``*_fwd`` and ``*_bwd`` are the plain calls, the names without a suffix
-are differentiable.  ``stream`` (default: torch's current stream) queues the call there, with its outputs allocated for
+are differentiable, once: a second derivative through them is an error.  ``stream`` (default: torch's current stream) queues the call there, with its outputs allocated for
 that stream; the caller orders it after the work that made the inputs.
 """
 from __future__ import annotations
@@ -17,6 +17,7 @@ from array import array
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import GdrError
@@ -216,6 +217,7 @@ class GatedNorm(torch.autograd.Function):
         return gated_norm_fwd(x, z, weight, **ctx.how)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, z, weight = ctx.saved_tensors
         d = gated_norm_bwd(_rows(dy, 2), x, z, weight, **ctx.how)
@@ -335,6 +337,7 @@ class AddNorm(torch.autograd.Function):
         return y, out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dres):
         out, weight, vec, x = ctx.saved_tensors
         d = add_norm_bwd(_rows(dy, 1), _rows(dres, 1), out, weight, ctx.scale if vec is None else vec, x=x, eps=ctx.eps)
@@ -461,6 +464,7 @@ class LinearRecurrence(torch.autograd.Function):
         return h, ht
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh, dht):
         x, g, h0, cu_seqlens, states = ctx.saved_tensors
         d = linrec_bwd(x, g, _rows(dh, 1), h0, dht.contiguous(), cu_seqlens, states, complement=ctx.complement)
