@@ -11,6 +11,7 @@ import math
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import GdrBwdArgs, GdrBwdDesc, GdrError, GdrFwdArgs, GdrWyArgs
@@ -206,7 +207,8 @@ def gdr_fwd(q, k, v, beta, g, h0=None, cu_seqlens=None, *, scale=None, BT=64, st
 class ChunkGatedDeltaRule(torch.autograd.Function):
     """o, ht = forward(q, k, v, beta, g, h0, cu_seqlens, scale, BT): the chunked gated delta rule with its
     exact backward, both on the GPU kernels.  Gradients flow to q, k, v, beta, g (raw log-gate) and h0;
-    the backward recomputes the chunk states from the inputs (nothing but the inputs is saved)."""
+    the backward recomputes the chunk states from the inputs (nothing but the inputs is saved).  It has no
+    derivative of its own: a second derivative is an error."""
 
     @staticmethod
     def forward(ctx, q, k, v, beta, g, h0=None, cu_seqlens=None, scale=None, BT=64):
@@ -227,6 +229,7 @@ class ChunkGatedDeltaRule(torch.autograd.Function):
         return out["o"], out["ht"]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, dht):
         q, k, v, beta, g, h0, cu_seqlens = ctx.saved_tensors
         plan = ctx.plan

@@ -5,6 +5,7 @@ import torch
 
 import block_util as U
 from chunked_gated_delta_09_gb300 import add_norm, gated_norm, linear_recurrence
+from chunked_gated_delta_09_gb300.ops import chunk_gated_delta_rule
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +36,10 @@ def test_linear_recurrence():
     gen = U.seeded(42)
     x = leaf(gen, 1, 20, 32)
     ask_twice(x, *linear_recurrence(x, U.gates(gen, 1, 20, 32)))
+
+
+def test_chunk_gated_delta_rule():
+    gen = U.seeded(43)
+    q, k, v = (leaf(gen, 1, 64, 2, 32) for _ in range(3))
+    beta, g = (torch.rand(1, 64, 2, generator=gen).cuda() for _ in range(2))
+    ask_twice(v, *chunk_gated_delta_rule(q, k, v, beta, -g))
