@@ -84,7 +84,6 @@ struct F4 {
 };
 __device__ __forceinline__ F4 fma4(F4 a, F4 b, F4 c) { return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)}; }
 __device__ __forceinline__ F4 mul4(F4 a, F4 b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
-__device__ __forceinline__ F4 add4(F4 a, F4 b) { return {add2(a.lo, b.lo), add2(a.hi, b.hi)}; }
 __device__ __forceinline__ F4 make4(float x, float y, float z, float w) { return {F2(x, y), F2(z, w)}; }
 
 // ---------------------------------------------------------------- maps
@@ -442,6 +441,7 @@ template <int ROWS, int S, int W> struct LinrecSmem {
     float carry[LR_CH];           // what enters the tile
     uint64_t full[S];             // a stage's rows are there
     Ends<ROWS> ends[2];
+    uint32_t again;               // the channels that go token by token
 };
 
 // A warp's copies of its own rows have arrived, but for the LEFT groups of them issued last.
@@ -450,12 +450,233 @@ template <int LEFT> __device__ __forceinline__ void own_rows_there() {
     __syncwarp();
 }
 
-__device__ __forceinline__ void init_barriers(uint64_t *full, int stages, Peers &peers) {
+__device__ __forceinline__ void init_barriers(uint64_t *full, int stages, Peers &peers, uint32_t &again) {
     if (threadIdx.x == 0) {
+        again = 0;
         for (int q = 0; q < stages; ++q) mbar_init(&full[q], 1);
         mbar_init(&peers.bar[0], 1);
         mbar_init(&peers.bar[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+}
+
+// ---------------------------------------------------------------- growth
+// The walk's maps need factors of at most 1, which decays have.  Gates above 0 grow: the factor of some rows then passes fp32,
+// and makes a nan of a state of 0 and of growth that later decays take back; a factor that underflowed has lost what
+// growth would bring back; and an infinite state times such a factor is a nan.  So the walk looks for groups that grow and for
+// tiles that are entered by an infinity or a nan, and marks their channels, without a value kept for it.  Where there are
+// marks, the cluster goes through its rows once more when the walk has ended, as the recurrence is written: a lane for
+// each channel, a warp for each range of rows, first for the range's map, its factor with the exponent apart, then for
+// the rows themselves.  Channels that do have a decay above 1 or an infinity keep what this gives.  Gates of at most 0 and
+// finite states mark nothing; the walk takes 0 to 3 % longer for looking.  32768 x 2048 bf16 with fp32 gates on both
+// sides of 0: forward 0.76 ms, backward 1.28 (one lane a channel from the first row to the last: 11 and 18 ms).
+struct Watch {
+    uint32_t *again;  // in shared memory, a bit for each channel
+    uint32_t channels;
+    __device__ __forceinline__ Watch(uint32_t &a, uint32_t c) : again(&a), channels(c) {}
+    __device__ __forceinline__ void factors(F2 a, F2 b) const {  // (a nan counts: infinity times 0)
+        float x, y, z, w;
+        a.get(x, y), b.get(z, w);
+        if (__builtin_expect(!(x <= 1.f) | !(y <= 1.f) | !(z <= 1.f) | !(w <= 1.f), 0)) atomicOr(again, channels);
+    }
+    __device__ __forceinline__ void entered(float s) const {  // by a lane for each channel
+        if (__builtin_expect(!(fabsf(s) < INFINITY), 0)) atomicOr(again, 1u << (threadIdx.x & 31));
+    }
+    // Before the cluster's last barrier: this CTA's marks to all.
+    __device__ __forceinline__ void tell(int size) const {
+        __syncthreads();
+        const uint32_t c = *again;
+        if (c && (int)threadIdx.x < size)
+            asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(in_cta(again, threadIdx.x)), "r"(c) : "memory");
+    }
+};
+
+// A map of one channel whose factor is m 2^e, m in [1, 2) or 0 or a nan.
+struct WideMap {
+    float m, b;
+    int e, how;  // CUTS: it forgets what came before; MET: growth or an infinity among its rows
+    static constexpr int CUTS = 1, MET = 2;
+    __device__ __forceinline__ void factor(float a) {
+        const bool up = a > 1.f;  // (neither product leaves fp32: a is below 2^128, and may be as small as 2^-127)
+        m *= up ? 0.25f * a : a, e += up ? 2 : 0;
+        if (m < 1.17549435e-38f) m *= 0x1p64f, e -= 64;
+        if (m > 0.f && m < INFINITY) {
+            const int x = (__float_as_int(m) >> 23) - 127;
+            m = __int_as_float(__float_as_int(m) - (x << 23)), e += x;
+        }
+    }
+    __device__ __forceinline__ float operator()(float s) const {
+        if (how & CUTS) return b;
+        float v = m * s;
+        for (int left = max(min(e, 400), -400); left;) {  // (towards the result from one side: no step passes it)
+            const int x = max(min(left, 100), -100);
+            v *= __int_as_float((x + 127) << 23), left -= x;
+        }
+        return v + b;
+    }
+};
+
+// The cluster's rows in ranges of whole blocks of LR_SAVE, one for each warp.
+struct Range {
+    int from, to, index, ranges;
+    __device__ __forceinline__ Range(const LinrecParams &p, int rank) {
+        const int warps = blockDim.x >> 5;
+        index = rank * warps + (int)(threadIdx.x >> 5), ranges = p.cluster * warps;
+        const int64_t blocks = (p.rows + LR_SAVE - 1) / LR_SAVE, n = (blocks + ranges - 1) / ranges * LR_SAVE;
+        from = (int)min((int64_t)p.rows, n * index), to = (int)min((int64_t)p.rows, n * (index + 1));
+    }
+};
+// Which rows of a block are the first or the last of a sequence: a bit for each.  By a whole warp.
+struct BlockEnds {
+    uint32_t heads, tails;
+    __device__ __forceinline__ BlockEnds(const LinrecParams &p, int first) {
+        const int row = first + (threadIdx.x & 31);
+        int a = -1, b = -1;
+        if (row < min(first + LR_SAVE, p.rows)) Ends<32>::sequence_of(p, row, a, b);
+        heads = __ballot_sync(0xffffffffu, a == row), tails = __ballot_sync(0xffffffffu, b == row + 1);
+        heads &= (1u << LR_SAVE) - 1, tails &= (1u << LR_SAVE) - 1;
+    }
+};
+// A channel's values in a block of rows; zeros (and decays of 1) past the last row, and for a channel that is none.
+template <typename T, typename G, bool COMP> struct Block {
+    float a[LR_SAVE], b[LR_SAVE], rest[COMP ? LR_SAVE : 1], x[COMP ? LR_SAVE : 1];
+    __device__ __forceinline__ void read(const LinrecParams &p, int first, int c, bool on) {
+        const T *xp = reinterpret_cast<const T *>(p.x) + c;
+        const G *gp = reinterpret_cast<const G *>(p.g) + c;
+#pragma unroll
+        for (int r = 0; r < LR_SAVE; r += 2) {
+            Pack<G, 2> g;
+            float v[2] = {};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int64_t row = first + r + j;
+                g.v[j] = to_out_t<G>(0.f);
+                if (on && row < p.rows) g.v[j] = gp[row * p.g_ts], v[j] = to_f32(xp[row * p.x_ts]);
+            }
+            F2 a2, r2;
+            decay2(gates(g), a2, r2);
+            float q[2];
+            a2.get(a[r], a[r + 1]), r2.get(q[0], q[1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                b[r + j] = COMP ? v[j] * q[j] : v[j];
+                if (COMP) rest[r + j] = q[j], x[r + j] = v[j];
+            }
+        }
+    }
+};
+// What enters a warp's range, from the maps of those before it (BACK: after it), and whether any of all has met something.
+template <bool BACK> __device__ __forceinline__ float enter_range(WideMap own, const Range &range, WideMap *maps, bool &met) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    maps[threadIdx.x] = own;
+    cluster_sync();
+    float s = 0.f, at = 0.f;
+    met = false;
+    for (int i = 0; i < range.ranges; ++i) {
+        const int q = BACK ? range.ranges - 1 - i : i;
+        if (q == range.index) at = s;
+        uint32_t m, b, e, how;
+        asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(m), "=r"(b), "=r"(e), "=r"(how)
+                     : "r"(in_cta(&maps[q % warps * 32 + lane], q / warps))
+                     : "memory");
+        const WideMap map = {__uint_as_float(m), __uint_as_float(b), (int)e, (int)how};
+        s = map(s);
+        met |= (how & WideMap::MET) || fabsf(s) == INFINITY;
+    }
+    cluster_sync();  // no CTA ends while another reads its maps
+    return at;
+}
+static_assert(sizeof(WideMap) == 16, "");
+
+// By all threads of the cluster.  maps: one for each thread, in shared memory.
+template <typename T, typename G, bool COMP>
+__device__ __noinline__ void forward_again(const LinrecParams &p, int rank, int c, bool on, WideMap *maps) {
+    const Range range(p, rank);
+    Block<T, G, COMP> v;
+    auto first_state = [&](int row) { return p.h0 && on ? p.h0[(int64_t)Ends<32>::sequence_of(p, row) * p.dim + c] : 0.f; };
+    WideMap map = {1.f, 0.f, 0, 0};
+    for (int first = range.from; first < range.to; first += LR_SAVE) {
+        const BlockEnds ends(p, first);
+        v.read(p, first, c, on);
+#pragma unroll
+        for (int r = 0; r < LR_SAVE; ++r) {
+            if (ends.heads >> r & 1) map.b = first_state(first + r), map.how |= WideMap::CUTS;
+            map.b = fmaf(v.a[r], map.b, v.b[r]);
+            map.factor(v.a[r]);
+            if (v.a[r] > 1.f || fabsf(map.b) == INFINITY) map.how |= WideMap::MET;
+        }
+    }
+    bool met;
+    float h = enter_range<false>(map, range, maps, met);
+    const bool write = on && met;
+    for (int first = range.from; first < range.to; first += LR_SAVE) {
+        const BlockEnds ends(p, first);
+        v.read(p, first, c, on);
+        if (write && p.states) p.states[(int64_t)(first / LR_SAVE) * p.dim + c] = h;
+#pragma unroll
+        for (int r = 0; r < LR_SAVE; ++r) {
+            if (ends.heads >> r & 1) h = first_state(first + r);
+            h = fmaf(v.a[r], h, v.b[r]);
+            if (!write || first + r >= p.rows) continue;
+            if (p.h) reinterpret_cast<T *>(p.h)[(int64_t)(first + r) * p.dim + c] = to_out_t<T>(h);
+            if (p.ht && (ends.tails >> r & 1)) p.ht[(int64_t)Ends<32>::sequence_of(p, first + r) * p.dim + c] = h;
+        }
+    }
+}
+
+template <typename T, typename G, bool COMP>
+__device__ __noinline__ void backward_again(const LinrecParams &p, int rank, int c, bool on, WideMap *maps) {
+    const Range range(p, rank);
+    Block<T, G, COMP> v;
+    auto of_sequence = [&](const float *q, int row) { return q && on ? q[(int64_t)Ends<32>::sequence_of(p, row) * p.dim + c] : 0.f; };
+    // lambda before the rows after are added, with the gradient of the last state on a sequence's last row
+    auto dh_at = [&](int row, bool tail) {
+        float d = on && row < p.rows ? to_f32(reinterpret_cast<const T *>(p.dh)[(int64_t)row * p.dh_ts + c]) : 0.f;
+        if (tail) d += of_sequence(p.dht, row);
+        return d;
+    };
+    auto entering = [&](int first) { return on ? p.states[(int64_t)(first / LR_SAVE) * p.dim + c] : 0.f; };
+    const int last = range.from + (range.to - range.from - 1) / LR_SAVE * LR_SAVE;  // block
+    WideMap map = {1.f, 0.f, 0, 0};
+    for (int first = last; first >= range.from && range.from < range.to; first -= LR_SAVE) {
+        const BlockEnds ends(p, first);
+        v.read(p, first, c, on);
+        if (!(ends.heads & 1) && fabsf(entering(first)) == INFINITY) map.how |= WideMap::MET;
+#pragma unroll
+        for (int r = LR_SAVE - 1; r >= 0; --r) {
+            const bool tail = ends.tails >> r & 1;
+            const float d = dh_at(first + r, tail), lam = tail ? d : d + map.b;
+            if (tail) map.how |= WideMap::CUTS;
+            map.b = v.a[r] * lam;
+            map.factor(v.a[r]);
+            if (v.a[r] > 1.f || fabsf(lam) == INFINITY) map.how |= WideMap::MET;
+        }
+    }
+    bool met;
+    float m = enter_range<true>(map, range, maps, met);
+    const bool write = on && met;
+    for (int first = last; first >= range.from && range.from < range.to; first -= LR_SAVE) {
+        const BlockEnds ends(p, first);
+        v.read(p, first, c, on);
+        float before[LR_SAVE], h = entering(first);
+#pragma unroll
+        for (int r = 0; r < LR_SAVE; ++r) {
+            if (ends.heads >> r & 1) h = of_sequence(p.h0, first + r);
+            before[r] = COMP ? h - v.x[COMP ? r : 0] : h;
+            h = fmaf(v.a[r], h, v.b[r]);
+        }
+#pragma unroll
+        for (int r = LR_SAVE - 1; r >= 0; --r) {
+            const bool tail = ends.tails >> r & 1;
+            const float d = dh_at(first + r, tail), lam = tail ? d : d + m;
+            m = v.a[r] * lam;
+            if (!write || first + r >= p.rows) continue;
+            const int64_t at = (int64_t)(first + r) * p.dim + c;
+            reinterpret_cast<T *>(p.dx)[at] = to_out_t<T>(COMP ? v.rest[COMP ? r : 0] * lam : lam);
+            reinterpret_cast<G *>(p.dg)[at] = to_out_t<G>(m * before[r]);
+            if (p.dh0 && (ends.heads >> r & 1)) p.dh0[(int64_t)Ends<32>::sequence_of(p, first + r) * p.dim + c] = m;
+        }
     }
 }
 
@@ -491,7 +712,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : 2)
             copies_issued();
         }
     };
-    init_barriers(sm.full, S, sm.peers);
+    init_barriers(sm.full, S, sm.peers, sm.again);
     check_sequences(p);
     int sa = 0, sb = 0;  // (warp 2) the sequence met last
     if (wid == 2) sm.ends[0].find(p, rank, sa, sb);
@@ -501,6 +722,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : 2)
     __syncwarp();
     empty_sequences(p, rank, cb, p.h0, p.ht);
     float walked = 0.f;  // (warp 1) the state that enters the cluster's rows
+    const Watch watch(sm.again, 0xfu << ch);
     for (int k = 0; k < p.supers; ++k) {
         const int buf = k & 1, tile = k * p.cluster + rank, first = group * R, row0 = tile * ROWS + first;
         const Ends<ROWS> &ends = sm.ends[buf];
@@ -538,6 +760,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : 2)
         else compose(Const<true>());
         put_pair(&sm.maps[group][ch], A.lo, B.lo);
         put_pair(&sm.maps[group][ch + 2], A.hi, B.hi);
+        watch.factors(A.lo, A.hi);
         __syncthreads();
         // the tile's rows are in registers: their place takes the tile S further on
         if (k + S < p.supers && (!VEC || threadIdx.x == 96)) fetch(k + S);
@@ -547,6 +770,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : 2)
         if (wid == 1) {
             wait_peers(&sm.peers.bar[buf], (k >> 1) & 1, p);
             sm.carry[lane] = sm.peers.entry(buf, rank, p.cluster, walked);
+            watch.entered(sm.carry[lane]);
         } else if (wid == 2) {
             if (k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile + p.cluster, sa, sb);
         }
@@ -575,7 +799,11 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 5 : 2)
             }
         }
     }
+    watch.tell(p.cluster);
     cluster_sync();  // no CTA ends while another may still write to it
+    if (const uint32_t again = sm.again)
+        forward_again<T, G, COMP>(p, rank, cb * LR_CH + lane, (again >> lane & 1) && cb * LR_CH + lane < p.dim,
+                                  reinterpret_cast<WideMap *>(dynamic));
 }
 
 // ---------------------------------------------------------------- backward
@@ -623,7 +851,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 6 : 3)
             copies_issued();
         }
     };
-    init_barriers(sm.full, 4, sm.peers);
+    init_barriers(sm.full, 4, sm.peers, sm.again);
     check_sequences(p);
     int sa = 0, sb = 0;
     if (wid == 2) sm.ends[0].find(p, tile_of(0), sa, sb);
@@ -637,6 +865,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 6 : 3)
     __syncwarp();
     empty_sequences(p, rank, cb, p.dht, p.dh0);
     float walked = 0.f;
+    const Watch watch(sm.again, 3u << ch);
     for (int k = 0; k < p.supers; ++k) {
         const int buf = k & 1, tile = tile_of(k), first = group * R, row0 = tile * ROWS + first;
         const Ends<ROWS> &ends = sm.ends[buf];
@@ -695,6 +924,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 6 : 3)
         if (tcuts) scan_maps<WARPS, WARPS, true, true>(sm.maps, tcuts, wid, lane, sm.total);
         else scan_maps<WARPS, WARPS, true, false>(sm.maps, tcuts, wid, lane, sm.total);
         sm.peers.template tell<WARPS>(buf, rank, p.cluster, sm.total, tcuts != 0);
+        watch.factors(A, A);
         // everybody is done with this tile's g and with x and dh of the tile before
         if (!VEC || threadIdx.x == 96) {
             if (k + 1 < p.supers) fetch_x(k + 1);
@@ -704,6 +934,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 6 : 3)
         if (wid == 1) {
             wait_peers(&sm.peers.bar[buf], (k >> 1) & 1, p);
             sm.carry[lane] = sm.peers.entry(buf, rank, p.cluster, walked);
+            watch.entered(sm.carry[lane]);
         } else if (wid == 2) {
             if (k + 1 < p.supers) sm.ends[buf ^ 1].find(p, tile - p.cluster, sa, sb);
         }
@@ -741,7 +972,11 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 4 ? 6 : 3)
         if (plain) finish(Const<false>());
         else finish(Const<true>());
     }
+    watch.tell(p.cluster);
     cluster_sync();
+    if (const uint32_t again = sm.again)
+        backward_again<T, G, COMP>(p, rank, cb * LR_CH + lane, (again >> lane & 1) && cb * LR_CH + lane < p.dim,
+                                   reinterpret_cast<WideMap *>(dynamic));
 }
 
 // ---------------------------------------------------------------- single tokens

@@ -97,6 +97,10 @@ size_t gdr_norm_workspace_bytes(int64_t rows, int64_t dim, int sums);
  * h0, ht [N, dim] fp32: the state before the first and after the last token of each sequence, h0 NULL means
  * zero, ht NULL not returned.  N = batch, or num_seqs when > 0 (varlen: batch 1, cu_seqlens as in gdr_bwd.h;
  * empty sequences give ht = h0).  batch * tokens is at most 2^30.
+ * Gates are taken to [-88, 88.3] (16-bit ones to [-88, 88]); below -87.7 a is 0.  What the decays of up to 256
+ * successive rows leave of a state below 2^-126 of it counts as zero.  Gates above 0 grow: channels that have
+ * such, or whose states become infinite, are followed token by token, several times slower; a state that becomes
+ * infinite may be a nan instead in the rest of a sequence that ends within 256 rows.
  * states, if not NULL: fp32 [ceil(batch tokens / GDR_LINREC_SAVE), dim], the state that enters each GDR_LINREC_SAVE
  * rows (of no meaning where a sequence starts on the first of them); the backward takes them.  h may be NULL (states and ht alone).
  * workspace: gdr_linrec_workspace_bytes(batch * tokens, dim) bytes, 256-byte aligned, not used by another call
