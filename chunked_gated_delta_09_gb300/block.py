@@ -18,6 +18,7 @@ from typing import Optional, Sequence
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from ._lib import GdrError
@@ -503,6 +504,7 @@ def linrec_step(x, g, state, slots=None, *, complement=False, stream=None) -> to
            _pack_linrec_step(x.data_ptr(), g.data_ptr(), _ptr(slots), state.data_ptr(), y.data_ptr(), B, D, state.shape[0],
                              _token_stride(x, "x"), _token_stride(g, "g"), _DT[x.dtype], _DT[g.dtype], int(complement), 0),
            index)
+    increment_version(state)  # (as torch's own in-place operations do: a backward that saved it notices)
     return y
 
 
@@ -539,6 +541,8 @@ def _clip(entry, grads: Sequence[torch.Tensor], max_norm, out, eps):
 
     _queue(entry, _pack_clip(addr(ptrs), addr(outs), addr(sizes), addr(types), addr(out_types), norm.data_ptr(),
                              ws.data_ptr(), len(grads), nbytes, max_norm, eps), index)
+    if out is not None or entry == "gdr_clip_grad_norm":
+        increment_version(grads if out is None else out)
     return norm
 
 
