@@ -509,28 +509,48 @@ def linrec_step(x, g, state, slots=None, *, complement=False, stream=None) -> to
 
 
 # ---------------------------------------------------------------- gradient norm and clip
+def _layout(t: torch.Tensor):
+    """(size, distance) of the axes that have more than one element."""
+    return [(n, s) for n, s in zip(t.shape, t.stride()) if n != 1]
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether the elements fill a stretch of memory, in whatever order of the axes."""
+    span = 1
+    for s, n in sorted((s, n) for n, s in _layout(t)):
+        if s != span:
+            return False
+        span *= n
+    return True
+
+
 def _listed(tensors, name, index):
-    """Addresses, sizes and types of a list of tensors as arrays for the C entry."""
+    """Addresses, sizes and types of a list of tensors as arrays for the C entry, and whether all are contiguous."""
     # (attribute by attribute: a list is checked in a fraction of the time that a loop over its tensors takes)
-    if [t.get_device() for t in tensors].count(index) != len(tensors) or not all([t.is_contiguous() for t in tensors]):
-        raise ValueError(f"{name} must be contiguous tensors on cuda:{index}")
+    flat = all([t.is_contiguous() for t in tensors])
+    if [t.get_device() for t in tensors].count(index) != len(tensors) or not (
+            flat or all([t.is_contiguous() or _dense(t) for t in tensors])):
+        raise ValueError(f"{name} must be tensors on cuda:{index} without gaps (contiguous, or with their axes permuted)")
     try:
         types = array("i", [_DT[t.dtype] for t in tensors])
     except KeyError:
         raise ValueError(f"{name} must be float32, bfloat16 or float16 tensors") from None
-    return array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors]), types
+    return array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors]), types, flat
 
 
 def _clip(entry, grads: Sequence[torch.Tensor], max_norm, out, eps):
     grads = list(grads)
     _need(len(grads) > 0, "no gradients were given")
     index = _cuda(grads[0], "grads[0]")
-    ptrs, sizes, types = _listed(grads, "grads", index)
+    ptrs, sizes, types, flat = _listed(grads, "grads", index)
     outs, out_types = None, None
     if out is not None:
         out = list(out)
-        outs, out_sizes, out_types = _listed(out, "out", index)
+        outs, out_sizes, out_types, out_flat = _listed(out, "out", index)
         _need(out_sizes == sizes, "out must have one tensor for each gradient, of its size")
+        if not (flat and out_flat):  # (element by element in the order of memory)
+            _need(all([_layout(o) == _layout(g) or (o.is_contiguous() and g.is_contiguous()) for g, o in zip(grads, out)]),
+                  "out must have its axes in the gradients' order in memory")
     dev = grads[0].device
     nbytes = _entry("gdr_clip_workspace_bytes")(len(grads), sum(sizes))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -547,8 +567,8 @@ def _clip(entry, grads: Sequence[torch.Tensor], max_norm, out, eps):
 
 
 def grad_norm(grads, *, stream=None) -> torch.Tensor:
-    """sqrt of the sum of all squares over a list of contiguous tensors (fp32, bf16, fp16 in any mixture, any of them
-    empty), as a 0-dim fp32 tensor."""
+    """sqrt of the sum of all squares over a list of tensors (fp32, bf16, fp16 in any mixture, any of them empty, without
+    gaps in memory: contiguous or with their axes permuted), as a 0-dim fp32 tensor."""
     if stream is not None:
         grads = list(grads)
         with _on(stream, grads):
@@ -558,7 +578,8 @@ def grad_norm(grads, *, stream=None) -> torch.Tensor:
 
 def clip_grad_norm(grads, max_norm, out=None, *, eps=1e-6, stream=None) -> torch.Tensor:
     """Scale the gradients by min(1, max_norm / (norm + eps)), in place or into ``out`` (a tensor for each, of any of the
-    types), and return their norm before that, as :func:`grad_norm` does.  Nothing is read back to the host."""
+    types, with its axes in the same order in memory), and return their norm before that, as :func:`grad_norm` does.
+    Nothing is read back to the host."""
     if stream is not None:
         grads, out = list(grads), None if out is None else list(out)
         with _on(stream, grads + (out or [])):

@@ -128,3 +128,26 @@ def test_a_tensor_beyond_32_bits():
     ref = ((n - 3) * 0.25 + 21.0) ** 0.5
     assert abs(float(norm) - ref) <= U.FP32_BAR * ref
     assert U.rel(g[-3:], torch.tensor([1.0, 2.0, -4.0], dtype=torch.float64) / (ref + 1e-6)) <= U.BAR[torch.bfloat16]
+
+
+def test_axes_may_be_permuted():
+    """Gradients of transposed and channels-last weights, in place and into tensors of their layout."""
+    gen = U.seeded(6)
+
+    def lists(dtype):
+        return [U.randn(gen, 30, 50, dtype=dtype).t(), U.randn(gen, 4, 6, 5, 3).to(dtype).to(memory_format=torch.channels_last),
+                U.randn(gen, 9, dtype=dtype), U.randn(gen, 7, 1, 4).to(dtype).permute(2, 1, 0)]
+
+    for dtype in (torch.float32, torch.bfloat16):
+        grads = lists(dtype)
+        assert not grads[0].is_contiguous() and not grads[3].is_contiguous()
+        check(grads, 1.0, [torch.full_like(t, float("nan"), dtype=torch.float32) for t in grads])
+        check(grads, 1.0)
+    grads, out = lists(torch.float32), lists(torch.float32)
+    for bad in (0, 1, 3):
+        with pytest.raises(ValueError):
+            clip_grad_norm(grads, 1.0, [t.contiguous() if i == bad else t for i, t in enumerate(out)])
+    with pytest.raises(ValueError):
+        grad_norm([U.randn(gen, 1, 8).expand(4, 8)])
+    with pytest.raises(ValueError):
+        grad_norm([U.randn(gen, 8, 8).t()[::2]])
