@@ -539,13 +539,17 @@ def _listed(tensors, name, index):
 
 
 def _clip(entry, grads: Sequence[torch.Tensor], max_norm, out, eps):
-    grads = list(grads)
+    grads, out = list(grads), None if out is None else list(out)
+    _need(out is None or len(out) == len(grads), "out must have one tensor for each gradient, of its size")
+    if any([t is None for t in grads]):
+        kept = [i for i, t in enumerate(grads) if t is not None]
+        grads, out = [grads[i] for i in kept], None if out is None else [out[i] for i in kept]
     _need(len(grads) > 0, "no gradients were given")
     index = _cuda(grads[0], "grads[0]")
     ptrs, sizes, types, flat = _listed(grads, "grads", index)
     outs, out_types = None, None
     if out is not None:
-        out = list(out)
+        _need(not any([t is None for t in out]), "out must have one tensor for each gradient, of its size")
         outs, out_sizes, out_types, out_flat = _listed(out, "out", index)
         _need(out_sizes == sizes, "out must have one tensor for each gradient, of its size")
         if not (flat and out_flat):  # (element by element in the order of memory)
@@ -568,7 +572,8 @@ def _clip(entry, grads: Sequence[torch.Tensor], max_norm, out, eps):
 
 def grad_norm(grads, *, stream=None) -> torch.Tensor:
     """sqrt of the sum of all squares over a list of tensors (fp32, bf16, fp16 in any mixture, any of them empty, without
-    gaps in memory: contiguous or with their axes permuted), as a 0-dim fp32 tensor."""
+    gaps in memory: contiguous or with their axes permuted), as a 0-dim fp32 tensor.  An entry may be None, as the
+    gradient of a weight that took no part is, but not all of them."""
     if stream is not None:
         grads = list(grads)
         with _on(stream, grads):

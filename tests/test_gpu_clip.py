@@ -151,3 +151,23 @@ def test_axes_may_be_permuted():
         grad_norm([U.randn(gen, 1, 8).expand(4, 8)])
     with pytest.raises(ValueError):
         grad_norm([U.randn(gen, 8, 8).t()[::2]])
+
+
+def test_weights_that_took_no_part_have_no_gradient():
+    gen = U.seeded(7)
+    a, b = U.randn(gen, 40), U.randn(gen, 5, 5)
+    n = norm64([a, b])
+    assert abs(float(grad_norm([None, a, None, b])) - n) <= U.FP32_BAR * n
+    out = [None, torch.empty_like(a), torch.full((3,), 7.0, device="cuda"), torch.empty_like(b)]
+    for stream in (None, torch.cuda.current_stream()):
+        clip_grad_norm([None, a, None, b], 1.0, out, stream=stream)
+        assert U.rel(out[1], U.f64(a) / (n + 1e-6)) <= U.FP32_BAR and U.rel(out[3], U.f64(b) / (n + 1e-6)) <= U.FP32_BAR
+        assert (out[2] == 7.0).all()
+    for call in (lambda: grad_norm([None, None]), lambda: clip_grad_norm([None], 1.0),
+                 lambda: clip_grad_norm([a, None], 1.0, [a]), lambda: clip_grad_norm([a], 1.0, [None])):
+        with pytest.raises(ValueError):
+            call()
+    x, unused = U.randn(gen, 8).requires_grad_(), U.randn(gen, 8).requires_grad_()
+    x.square().sum().backward()
+    clip_grad_norm([p.grad for p in (x, unused)], 1.0)
+    assert abs(float(x.grad.norm()) - 1.0) <= U.FP32_BAR
