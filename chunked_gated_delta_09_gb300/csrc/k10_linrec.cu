@@ -87,7 +87,8 @@ cudaError_t linrec_plan(LinrecParams &p, LinrecLaunch &l, int rows_per_tile, boo
 
 cudaError_t linrec_maps(const LinrecParams &p, LinrecMaps &maps, int rows_per_tile) {
     auto one = [&](CUtensorMap &map, const void *base, int dtype, int64_t stride) {
-        return encode_matrix_map(&map, base, dtype, p.rows, p.dim, p.rows > 1 ? stride : p.dim, rows_per_tile, LR_CH);
+        // (one row has no distance to a next one: any that a map takes)
+        return encode_matrix_map(&map, base, dtype, p.rows, p.dim, p.rows > 1 ? stride : (p.dim + 7) / 8 * 8, rows_per_tile, LR_CH);
     };
     cudaError_t e = one(maps.g, p.g, p.gate_dtype, p.g_ts);
     if (e == cudaSuccess) e = one(maps.x, p.x, p.dtype, p.x_ts);

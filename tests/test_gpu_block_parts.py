@@ -128,3 +128,27 @@ def test_gated_norm(tokens, heads, dim, dtype):
                 assert (got[name] == 77.0).all()
                 ref.pop(name)
         U.check(got, ref)
+
+
+@pytest.mark.parametrize("dtype,gtype", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("T,D", [(1, 4), (1, 12), (1, 7), (2, 4), (17, 20), (300, 36), (300, 33)])
+def test_recurrence_forward(T, D, dtype, gtype):
+    """h, ht and states absent or not."""
+    gen, dt, gt, ts = U.seeded(T + D), TYPES[dtype], TYPES[gtype], wide(D)
+    x, g = padded(gen, T, D, ts, dt), padded(gen, T, D, ts, gt)
+    g.copy_(-g.abs())
+    ref = U.linrec(x[None], g[None], None, None, False)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    saved = torch.cat([torch.zeros(1, D, dtype=torch.float64), ref["h"][0, 15::16]])[:-(-T // 16)]
+    for parts in itertools.product((False, True), repeat=3):
+        h, ht, states = Guarded(T * D, dt), Guarded(D, torch.float32), Guarded(-(-T // 16) * D, torch.float32)
+        call("gdr_linrec_fwd", _lib.GdrLinrecFwdArgs, x=x.data_ptr(), g=g.data_ptr(), h=h.ptr() if parts[0] else None,
+             ht=ht.ptr() if parts[1] else None, states=states.ptr() if parts[2] else None, workspace=ws.data_ptr(), batch=1,
+             tokens=T, dim=D, x_token_stride=ts, g_token_stride=ts, workspace_bytes=256, dtype=CODE[dt], gate_dtype=CODE[gt])
+        want = dict(h=ref["h"][0], ht=ref["ht"][0], states=saved[1:])
+        got = dict(h=h.value(T, D), ht=ht.value(D), states=states.value(-1, D)[1:])
+        for on, name in zip(parts, ("h", "ht", "states")):
+            if not on:
+                assert (got.pop(name) == 77.0).all()
+                want.pop(name)
+        U.check(got, want)
