@@ -15,12 +15,12 @@
 // tile arrives by tensor-map loads meanwhile.  The forward saves the state that enters each LR_SAVE rows (a warp's rows of
 // the backward), from which the backward recomputes h instead of reading it back rounded.
 //
-// Measured: 32768 x 2048 bf16 with fp32 gates forward 0.093 ms (5.8 TB/s of the 6.8 of a plain copy), backward 0.167 ms
-// (5.2); 48763 x 4096 bf16 with 1 - a, packed, forward 0.274 ms (4.4), backward 0.487 ms (4.2); 30000 x 16384 forward
-// 0.528 ms (5.6).  Bytes do not bind it yet but, SM by SM, the instructions (24 to an element, backwards 42, half of them the
+// Measured: 32768 x 2048 bf16 with fp32 gates forward 0.096 ms (5.6 TB/s of the 6.8 of a plain copy), backward 0.164 ms
+// (5.8); 48763 x 4096 bf16 with 1 - a, packed, forward 0.280 ms (4.3), backward 0.486 ms (4.2); 30000 x 16384 forward
+// 0.533 ms (5.5).  Bytes do not bind it yet but, SM by SM, the instructions (24 to an element, backwards 43, half of them the
 // exponential) between the two barriers of a tile and the cluster's exchange.  Widths of 2048 or 4096 make 64 or 128 blocks
 // of channels, whose clusters fill 93 or 84 % of the SMs' places.  CTAs of 4 warps, of which an SM holds five (backwards five or six),
-// hide the exchange best: 8 warps take 0.310 ms where 4 take 0.289 and 2 take 0.302 (48763 x 4096, forward).
+// hide the exchange best: 8 warps took 0.310 ms where 4 took 0.289 and 2 took 0.302 (48763 x 4096, forward, an earlier state).
 #pragma once
 
 #include "block_common.cuh"
@@ -37,14 +37,16 @@ constexpr int LR_R = 8;                       // rows of a group
 constexpr int LR_FWD_PER = 4, LR_BWD_PER = 2;  // groups of a warp
 static_assert(LR_SAVE == LR_BWD_PER * LR_R, "a saved state enters each warp's rows of the backward");
 
-// exp(g) and 1 - exp(g), both to about one unit in the last place and without a lean to one side, which a channel that
-// remembers hundreds of tokens would add up (decays near 1 that come out a quarter of a unit too low put h off by
-// 1e-5).  Cody and Waite's reduction g = n ln 2 + r, then exp(r) - 1 = r + r^2 q(r) with q a Chebyshev fit of degree 4
-// (1e-8 off), so that 1 - a is exact to rounding near a = 1.  Below -87.7 a is 0; above 88.3 it is taken at 88.3.
+// exp(g) and 1 - exp(g).  Near a = 1 both are right to rounding and without a lean to one side, which a channel that
+// remembers hundreds of tokens would add up (decays near 1 that come out a quarter of a unit too low put h off by 1e-5).
+// Cody and Waite's reduction g = n ln 2 + r, then exp(r) - 1 = r + r^2 q(r) with q a Chebyshev fit of degree 4 (1e-8 off).
+// ln 2 is one constant, 1.9e-9 off, which n times leans further out, where a state is soon forgotten.  a is off, in units of
+// 2^-24, at most and on average: gates in [-1, 0] 1.3, 0.0; [-10, -1] 1.6, 0.3; [-40, -10] 3.1, 1.2; [-87, -40] 5.2, 2.9; [0, 1]
+// 1.3, 0.0; [1, 10] 1.6, -0.3; [10, 88] 5.2, -2.3.  Below -87.7 a is 0; above 88.3 it is taken at 88.3.
 __device__ __forceinline__ void decay2(F2 g, F2 &a, F2 &rest) {
     const F2 shift(12582912.f), one(1.f);  // 1.5 x 2^23: the sum's low bits are the rounded integer
     const F2 t = fma2(g, F2(1.44269504f), shift), n = add2(t, F2(-12582912.f));
-    const F2 r = fma2(n, F2(-0.693147181f), g);  // (ln 2 is 1.9e-9 off: n times that, below a rounding of a until a < 1e-9)
+    const F2 r = fma2(n, F2(-0.693147181f), g);  // (ln 2 is 1.9e-9 off: n times that, a rounding of a at a = 1e-9)
     F2 q = fma2(r, F2(0.0013933823f), F2(0.0083632953f));
     q = fma2(q, r, F2(0.041666463f));
     q = fma2(q, r, F2(0.16666576f));
@@ -308,7 +310,7 @@ template <typename T, int ROWS> struct Tile {
     }
     // Where the rows cannot be moved by a tensor map a warp brings its own N: by asynchronous copies of pieces, or 16 single
     // elements at a time where those have 16 bits and nothing larger is aligned (32768 x 2052 bf16 with fp32 gates forward
-    // 0.189 ms, 2050 0.196, 2049 0.264; by registers, 16 loads at a time, 0.265, 0.297 and 0.323).
+    // 0.189 ms, 2050 0.197, 2049 0.267; by registers, 16 loads at a time, 0.265, 0.297 and 0.323).
     template <int N>
     __device__ __forceinline__ void bring(const void *src, int64_t ts, int piece, int tile, int wid, int cb, const LinrecParams &p) {
         const T *from = reinterpret_cast<const T *>(src);
@@ -1012,7 +1014,7 @@ template <typename T, typename G, int V, bool COMP> __global__ void __launch_bou
 }  // namespace
 
 // Few blocks of channels leave the SMs with one or two CTAs each, which then wait for each tile: CTAs of 8 warps take twice
-// the rows to a tile (65536 x 512 bf16 forward 0.069 ms, backward 0.133; 4 warps 0.085, 0.155).
+// the rows to a tile (65536 x 512 bf16 forward 0.072 ms, backward 0.132; 4 warps 0.085, 0.155).
 #define RUN(KERNEL, STAGES, WARPS, COMP, VEC)                                                       \
     do {                                                                                            \
         auto kernel = KERNEL<T, G, WARPS, COMP, VEC>;                                               \

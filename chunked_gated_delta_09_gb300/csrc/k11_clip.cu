@@ -9,7 +9,7 @@
 // the two, and scales.  Both are bound by HBM: the gradients have to be read twice, since all of them decide on the
 // factor.  The second kernel goes through the pieces from the last to the first, whose end is then still in L2.
 // 393 million bf16 gradients clipped into fp32: 0.484 ms, 6.5 TB/s (6.8 is a plain copy's).  A few small tensors are one
-// launch (k11_small): clipping 20 of them takes 40 us, nearly all of it the host's work on the list.
+// launch (k11_small).
 //
 // Squares are summed in fp32 within a thread's part of a piece (at most 32 of them to a sum) and in fp64 from there on.
 #include "block_clip.h"
@@ -151,7 +151,8 @@ __device__ __forceinline__ void cluster_meet() {
 }
 
 // Both steps in one launch, by one cluster whose CTAs tell each other their partial sums: for small totals, where a second
-// launch costs more than the work (20 fp32 tensors of 4096: 41 -> 32 us a call, host included).
+// launch costs more than the work (20 fp32 tensors of 4096: 9 us of a call less; it takes 35 to 40, nearly all of it the host's
+// work on the list).
 template <int N, bool SCALE>
 __global__ void __launch_bounds__(CLIP_THREADS) k11_small(const __grid_constant__ ClipTable<N> t, float *norm, float max_norm,
                                                           float eps) {

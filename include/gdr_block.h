@@ -161,7 +161,9 @@ gdr_status gdr_linrec_step(const gdr_linrec_step_args *args, void *stream);
  * tensors themselves are contiguous device memory and may be empty.  outs NULL: in place (out_dtypes unused);
  * an entry of outs may be the same entry of grads when the types agree.  norm: one fp32 on the device.
  * A norm that is not finite gives what the formula gives: all finite gradients become 0 for an infinite norm,
- * everything becomes nan for a nan norm.  gdr_grad_norm computes the norm alone.
+ * everything becomes nan for a nan norm.  Squares are formed in fp32 and added in fp32 32 at a time, in fp64 from there:
+ * a value above 1.8e19 makes the norm infinite, values below 1e-23 count as zero.  gdr_grad_norm computes the norm
+ * alone.
  * workspace: gdr_clip_workspace_bytes(count, total number of elements) bytes, 16-byte aligned. */
 typedef struct {
     const void *const *grads;

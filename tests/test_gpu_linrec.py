@@ -370,3 +370,27 @@ def test_malformed_lists_of_many_sequences_are_reported():
                 call()
             assert e.value.status == _lib.GDR_ERR_DEVICE
     linrec_fwd(p["x"], p["g"], p["h0"], p["cu_seqlens"], check_status=True)
+
+
+@pytest.mark.parametrize("lo,hi", [(-1, 0), (-10, -1), (-40, -10), (-87, -40), (0, 1), (1, 10), (10, 88)])
+def test_decays_by_themselves(lo, hi):
+    """exp(g) and 1 - exp(g) as a step on a state of 1 and on an input of 1 shows them.
+
+    In units of 2^-24 of a: its own rounding 1, those before it 0.25 each for p, r and 1 + p's share, the polynomial 0.2: below
+    2; and n times the constant's 1.9e-9, which is 0.033 for each n = g / ln 2.  Near 1 both signs are as frequent: the
+    mean of a million is below 0.1.  1 - a for decays: its rounding 1 and what a has, times a / (1 - a) <= 2.4 outside the
+    polynomial's own range: below 4 plus the same n, of which a / (1 - a) leaves less than half a unit."""
+    g = (torch.rand(1024, 1024, generator=U.seeded(33), dtype=torch.float64) * (hi - lo) + lo).float().cuda()
+    state = torch.ones_like(g)
+    linrec_step(torch.zeros_like(g), g, state)
+    a = torch.exp(g.double())
+    off = (state.double() - a) / a * 2.0 ** 24
+    assert float(off.abs().max()) <= 2.0 + 0.033 * max(abs(lo), abs(hi)) / 0.693
+    if abs(lo) <= 1 and abs(hi) <= 1:
+        assert abs(float(off.mean())) <= 0.1
+    if hi <= 0:
+        rest = torch.zeros_like(g)
+        linrec_step(torch.ones_like(g), g, rest, complement=True)
+        want = -torch.expm1(g.double())
+        seen = want > 0  # (a gate of exactly 0 leaves nothing)
+        assert float(((rest.double() - want)[seen] / want[seen]).abs().max()) <= 4.5 * 2.0 ** -24
