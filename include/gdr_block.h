@@ -11,7 +11,7 @@
  *
  * Rows: the last axis of every tensor is contiguous; a "token stride" or "head stride" is the distance in
  * elements from one token or head to the next.  Pointers are aligned to their element type.  Rows whose
- * pointers and strides are multiples of 16 bytes are moved in 16-byte pieces, others element by element (by
+ * pointers, strides and widths are multiples of 16 bytes are moved in 16-byte pieces, others element by element (by
  * the recurrence in pieces of 4 or 2 elements where those are aligned).
  * Outputs without a stride argument are contiguous.  Inputs and outputs must not overlap unless said.
  * A call with no tokens (or no elements) is valid: sums over tokens are then zero.

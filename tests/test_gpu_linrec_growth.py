@@ -157,3 +157,35 @@ def test_an_infinite_state_stays_infinite(D):
     assert (back["dx"][0, :1401, 9] == float("inf")).all()
     others = [c for c in range(D) if c != 9]
     assert all(torch.equal(back[k][..., others], ref[k][..., others]) for k in ref)
+
+
+@pytest.mark.parametrize("B,rows,down,D", [(3, 2, 3, 40), (5, 2, 2, 33), (2, 70, 90, 64), (4, 150, 700, 40)])
+@pytest.mark.parametrize("complement", [False, True], ids=["plain", "complement"])
+def test_batches_and_rows_at_a_distance(B, rows, down, D, complement):
+    """Sequences side by side, shorter than a range of rows or longer, x, g and dh as columns of wider rows."""
+    parts = [rise_and_fall(rows, down, 1, D, torch.float32, torch.float32, seed=80 + b) for b in range(B)]
+    p = {k: torch.cat([a[k] for a, _ in parts]) for k in ("x", "g", "h0")}
+    d = {k: torch.cat([b[k] for _, b in parts]) for k in ("dh", "dht")}
+    for name, where in (("x", p), ("g", p), ("dh", d)):
+        wide = torch.full((*where[name].shape[:2], D + 5), float("nan"), device="cuda")
+        wide[..., 2:2 + D] = where[name]
+        where[name] = wide[..., 2:2 + D]
+    bar = 8 * p["x"].shape[1] * 2.0 ** -24
+    h, ht, states = linrec_fwd(p["x"], p["g"], p["h0"], complement=complement, return_states=True, check_status=True)
+    got = linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], states=states, complement=complement, check_status=True)
+    ref = U.linrec(p["x"], p["g"], p["h0"], None, complement, d["dh"], d["dht"])
+    close(h, ref["h"], bar)
+    close(ht, ref["ht"], bar)
+    for name in ("dx", "dg", "dh0"):
+        close(got[name], ref[name], 3 * bar)
+
+
+def test_results_repeat_bit_for_bit():
+    p, d = rise_and_fall(140, 140, 6, 96, torch.bfloat16, torch.float32, seed=90)
+    first = None
+    for _ in range(5):
+        h, ht, states = linrec_fwd(p["x"], p["g"], p["h0"], return_states=True)
+        got = linrec_bwd(p["x"], p["g"], d["dh"], p["h0"], d["dht"], None, states)
+        now = [h, ht, states, *got.values()]
+        first = first or now
+        assert all(torch.equal(a, b) for a, b in zip(first, now))
