@@ -541,16 +541,21 @@ def _listed(tensors, name, index):
 def _clip(entry, grads: Sequence[torch.Tensor], max_norm, out, eps):
     grads, out = list(grads), None if out is None else list(out)
     _need(out is None or len(out) == len(grads), "out must have one tensor for each gradient, of its size")
-    if any([t is None for t in grads]):
-        kept = [i for i, t in enumerate(grads) if t is not None]
-        grads, out = [grads[i] for i in kept], None if out is None else [out[i] for i in kept]
     _need(len(grads) > 0, "no gradients were given")
-    index = _cuda(grads[0], "grads[0]")
-    ptrs, sizes, types, flat = _listed(grads, "grads", index)
+    try:
+        index = _cuda(grads[0], "grads[0]")
+        ptrs, sizes, types, flat = _listed(grads, "grads", index)
+    except AttributeError:  # (None has no device; looking for it first would cost every call)
+        kept = [i for i, t in enumerate(grads) if t is not None]
+        if len(kept) == len(grads):
+            raise
+        return _clip(entry, [grads[i] for i in kept], max_norm, None if out is None else [out[i] for i in kept], eps)
     outs, out_types = None, None
     if out is not None:
-        _need(not any([t is None for t in out]), "out must have one tensor for each gradient, of its size")
-        outs, out_sizes, out_types, out_flat = _listed(out, "out", index)
+        try:
+            outs, out_sizes, out_types, out_flat = _listed(out, "out", index)
+        except AttributeError:
+            raise ValueError("out must have one tensor for each gradient, of its size") from None
         _need(out_sizes == sizes, "out must have one tensor for each gradient, of its size")
         if not (flat and out_flat):  # (element by element in the order of memory)
             _need(all([_layout(o) == _layout(g) or (o.is_contiguous() and g.is_contiguous()) for g, o in zip(grads, out)]),
