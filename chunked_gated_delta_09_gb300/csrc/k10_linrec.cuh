@@ -504,13 +504,14 @@ struct WideMap {
         if (m < 1.17549435e-38f) m *= 0x1p64f, e -= 64;
         if (m > 0.f && m < INFINITY) {
             const int x = (__float_as_int(m) >> 23) - 127;
-            m = __int_as_float(__float_as_int(m) - (x << 23)), e += x;
+            m = __int_as_float(__float_as_int(m) - (x << 23));
+            e = max(min(e + x, 1 << 28), -(1 << 28));  // (far beyond what any state comes back from)
         }
     }
     __device__ __forceinline__ float operator()(float s) const {
         if (how & CUTS) return b;
-        float v = m * s;
-        for (int left = max(min(e, 400), -400); left;) {  // (towards the result from one side: no step passes it)
+        float v = 0.5f * m * s;  // (at most s)
+        for (int left = max(min(e + 1, 400), -400); left;) {  // (towards the result from one side: no step passes it)
             const int x = max(min(left, 100), -100);
             v *= __int_as_float((x + 127) << 23), left -= x;
         }

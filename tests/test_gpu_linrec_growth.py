@@ -189,3 +189,22 @@ def test_results_repeat_bit_for_bit():
         now = [h, ht, states, *got.values()]
         first = first or now
         assert all(torch.equal(a, b) for a, b in zip(first, now))
+
+
+def test_states_beside_the_largest_number():
+    """States (forward) and their gradients (backward) of up to 3e38 that the decays of a range take down a little."""
+    D, up, down = 40, 176, 500
+    g = torch.cat([torch.full((up, D), 0.5), torch.full((down, D), -0.01)])[None].cuda()
+    h0 = (1.6 + 0.4 * torch.rand(1, D, generator=U.seeded(91))).cuda()
+    zero = torch.zeros_like(g)
+    bar = 8 * (up + down) * 2.0 ** -24
+    h, ht, states = linrec_fwd(zero, g, h0, return_states=True)
+    ref = U.linrec(zero, g, h0, None, False)
+    assert 2.5e38 < float(ref["h"].max()) < 3.4e38
+    close(h, ref["h"], bar)
+    close(ht, ref["ht"], bar)
+    back = g.flip(1).contiguous()
+    got = linrec_bwd(zero, back, zero, None, h0)
+    ref = U.linrec(zero, back, None, None, False, zero, h0)
+    close(got["dx"], ref["dx"], bar)
+    close(got["dh0"], ref["dh0"], bar)
