@@ -97,7 +97,8 @@ struct FfnPad {
     void *to[3];
     int64_t stride[3], rows[3];
     uint32_t warps[3];
-    int count, cols, pitch;
+    int count, cols;
+    int64_t pitch;  // (64 bits: rows times pitch passes 2^32)
     FastDiv per_row;
     int *status;  // cleared
 };

@@ -239,3 +239,48 @@ def test_offsets_beyond_32_bits():
     f = F.forward(x, wg[part], wu[part], "silu")
     want = F.backward(dh[:, part], x, wg[part], wu[part], f["gate"], f["up"], "silu")
     F.check({n: d[n][part] for n in ("dw_gate", "dw_up")}, {n: want[n] for n in ("dw_gate", "dw_up")}, times=2)
+
+
+# Rows that are copied to 16-byte boundaries, of more than 2^32 elements in all: the first row past it, its neighbours, and the rows
+# that an offset of 32 bits would take for those.
+LONG, ODD = 1048000, 4097
+PAST = -(-2 ** 32 // 4104)
+AROUND = [0, 1, PAST - 1, PAST, PAST + 1, LONG - PAST - 1, LONG - PAST, LONG - 1]
+
+
+def test_copied_tokens_beyond_32_bits():
+    inner = 24
+    _, wg, wu, _ = F.inputs(18, 1, ODD, inner, BF16)
+    x = torch.randn(LONG, ODD, dtype=BF16, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    dh = torch.randn(LONG, inner, dtype=BF16, device="cuda", generator=torch.Generator("cuda").manual_seed(4))
+    h, saved = gated_ffn_fwd(x, wg, wu, return_saved=True, check_status=True)
+    rows = torch.tensor(AROUND, device="cuda")
+    for some in (rows, slice(0, 256), slice(PAST - 128, PAST + 128), slice(LONG - 256, LONG)):
+        F.check(dict(h=h[some], gate=saved[0][some], up=saved[1][some]), F.forward(x[some], wg, wu, "silu"))
+    d = gated_ffn_bwd(dh, x, wg, wu, saved, check_status=True)
+    want = F.backward(dh[rows], x[rows], wg, wu, saved[0][rows], saved[1][rows], "silu")
+    F.check(dict(dx=d["dx"][rows]), dict(dx=want["dx"]), times=2)
+    sums = {n: torch.zeros(inner, ODD, dtype=torch.float64, device="cuda") for n in ("dw_gate", "dw_up")}
+    for i in range(0, LONG, 1 << 17):
+        some = slice(i, i + (1 << 17))
+        part = F.backward(dh[some], x[some], wg, wu, saved[0][some], saved[1][some], "silu")
+        for n in sums:
+            sums[n] += part[n]
+    F.check({n: d[n] for n in sums}, sums, times=2)
+
+
+def test_copied_weights_beyond_32_bits():
+    tokens = 40
+    x, _, _, _ = F.inputs(19, tokens, ODD, 1, BF16)
+    wg, wu = (torch.randn(LONG, ODD, dtype=BF16, device="cuda", generator=torch.Generator("cuda").manual_seed(s)).mul_(ODD ** -0.5)
+              for s in (5, 6))
+    dh = torch.randn(tokens, LONG, dtype=BF16, device="cuda", generator=torch.Generator("cuda").manual_seed(7))
+    h, saved = gated_ffn_fwd(x, wg, wu, return_saved=True, check_status=True)
+    for some in (torch.tensor(AROUND, device="cuda"), slice(0, 256), slice(PAST - 128, PAST + 128), slice(LONG - 256, LONG)):
+        F.check(dict(h=h[:, some], gate=saved[0][:, some], up=saved[1][:, some]), F.forward(x, wg[some], wu[some], "silu"))
+    d = gated_ffn_bwd(dh, x, wg, wu, saved, need_dw=False, check_status=True)
+    want = torch.zeros(tokens, ODD, dtype=torch.float64, device="cuda")
+    for i in range(0, LONG, 1 << 17):
+        some = slice(i, i + (1 << 17))
+        want += F.backward(dh[:, some], x, wg[some], wu[some], saved[0][:, some], saved[1][:, some], "silu")["dx"]
+    F.check(dict(dx=d["dx"]), dict(dx=want), times=2)
