@@ -95,7 +95,7 @@ def gated_ffn_bwd(dh, x, w_gate, w_up, saved=None, *, activation="silu", need_dx
     shape = (*x.shape[:-1], inner)
     _like(dh, "dh", index, shape, x.dtype)
     if saved is None:
-        _, saved = gated_ffn_fwd(x, w_gate, w_up, activation=activation, return_saved=True)
+        _, saved = gated_ffn_fwd(x, w_gate, w_up, activation=activation, return_saved=True, check_status=check_status)
     _like(saved, "saved", index, (2, *shape), _F32)
     _need(saved.is_contiguous(), "saved must be contiguous")
     gate = saved.data_ptr()

@@ -4,7 +4,7 @@ import torch
 
 import block_util as U
 import ffn_util as F
-from chunked_gated_delta_09_gb300 import GdrError, _lib, gated_ffn, gated_ffn_bwd, gated_ffn_fwd
+from chunked_gated_delta_09_gb300 import GdrError, _lib, ffn, gated_ffn, gated_ffn_bwd, gated_ffn_fwd
 from chunked_gated_delta_09_gb300.ffn import _pack_bwd, _pack_fwd
 
 pytestmark = pytest.mark.gpu
@@ -284,3 +284,23 @@ def test_copied_weights_beyond_32_bits():
         some = slice(i, i + (1 << 17))
         want += F.backward(dh[:, some], x, wg[some], wu[some], saved[0][:, some], saved[1][:, some], "silu")["dx"]
     F.check(dict(dx=d["dx"]), dict(dx=want), times=2)
+
+
+def test_projections_computed_again_report_their_waits(monkeypatch):
+    x, wg, wu, dh = F.inputs(20, 600, 512, 512, BF16)
+    want = gated_ffn_bwd(dh, x, wg, wu, check_status=True)
+
+    def short(*args, **kwargs):  # the limit holds for the forward pass inside the call alone
+        monkeypatch.setenv("GDR_SPIN_LIMIT", "1")
+        try:
+            return gated_ffn_fwd(*args, **kwargs)
+        finally:
+            monkeypatch.delenv("GDR_SPIN_LIMIT")
+
+    with monkeypatch.context() as m:
+        m.setattr(ffn, "gated_ffn_fwd", short)
+        with pytest.raises(GdrError) as e:
+            gated_ffn_bwd(dh, x, wg, wu, check_status=True)
+        assert e.value.status == _lib.GDR_ERR_TIMEOUT
+    again = gated_ffn_bwd(dh, x, wg, wu, check_status=True)
+    assert all(torch.equal(again[n], want[n]) for n in want)
