@@ -8,6 +8,7 @@ that follows a gated feed-forward is one plain matrix product: ``gated_ffn(x, w_
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib
@@ -131,13 +132,19 @@ class GatedFfn(torch.autograd.Function):
         return d["dx"], d["dw_gate"], d["dw_up"], None
 
 
+def _dual(*tensors) -> bool:
+    """Whether any has a tangent of forward-mode differentiation (which no tensor has outside a level of it)."""
+    return getattr(forward_ad, "_current_level", 0) >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def gated_ffn(x, w_gate, w_up, *, activation="silu") -> torch.Tensor:
-    """Differentiable :func:`gated_ffn_fwd`; nothing is kept where no gradient is wanted.
+    """Differentiable :func:`gated_ffn_fwd`; nothing is kept where no gradient is wanted.  Tangents of forward-mode
+    differentiation are refused.
 
     A backward pass captured into a CUDA graph: as for every differentiable function, torch adds a leaf's gradients on the
     stream of that leaf's first use that is still alive.  Nothing that an earlier, eager pass over the same leaves gave may
     live then (losses and outputs with their graph dropped, as torch's own captures want it); ``gated_ffn_fwd`` and
     ``gated_ffn_bwd`` know no leaves and can be captured at any time."""
-    if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad):
+    if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad) or _dual(x, w_gate, w_up):
         return GatedFfn.apply(x, w_gate, w_up, activation)
     return gated_ffn_fwd(x, w_gate, w_up, activation=activation)

@@ -304,3 +304,16 @@ def test_projections_computed_again_report_their_waits(monkeypatch):
         assert e.value.status == _lib.GDR_ERR_TIMEOUT
     again = gated_ffn_bwd(dh, x, wg, wu, check_status=True)
     assert all(torch.equal(again[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("grad", [True, False])
+def test_forward_mode_is_refused(which, grad):
+    parts = list(F.inputs(21, 5, 16, 24, BF16)[:3])
+    with torch.set_grad_enabled(grad), torch.autograd.forward_ad.dual_level():
+        want = gated_ffn(*parts)  # no tangents: as without the level
+        dual = list(parts)
+        dual[which] = torch.autograd.forward_ad.make_dual(parts[which], torch.ones_like(parts[which]))
+        with pytest.raises(NotImplementedError):
+            gated_ffn(*dual)
+    assert torch.equal(gated_ffn(*parts), want)
