@@ -64,8 +64,10 @@ struct FfnGemm {
     float *part;       // partial results: a tile's rows of 256 for each part of each tile that is cut
     int dtype, act;
     uint32_t spin;
-    int *status;  // or null: nobody asks
-    bool clear;  // the kernel's first CTA clears the status word: no other can have run out of polls before it has begun
+    // Whether waits ran out: a byte for each CTA, which no other writes, so that clearing needs no order among them; or null: nobody
+    // asks.  clear: what the bytes held is of an earlier call (else an earlier launch of this call has cleared them).
+    uint8_t *status;
+    bool clear;
 };
 cudaError_t launch_ffn_product(const FfnMaps &maps, const FfnGemm &p, cudaStream_t stream);
 
@@ -87,7 +89,7 @@ struct FfnAct {
     int64_t dh_ts, tokens, inner, pitch;
     int dtype, act;
     bool vec;
-    int *status;  // cleared
+    uint8_t *status;  // cleared
 };
 cudaError_t launch_ffn_act(const FfnAct &p, cudaStream_t stream);
 
@@ -100,7 +102,7 @@ struct FfnPad {
     int count, cols;
     int64_t pitch;  // (64 bits: rows times pitch passes 2^32)
     FastDiv per_row;
-    int *status;  // cleared
+    uint8_t *status;  // cleared
 };
 cudaError_t launch_ffn_pad(FfnPad p, cudaStream_t stream);
 

@@ -26,7 +26,7 @@ bool mappable(const void *p, int64_t stride, int64_t rows, int64_t cols) {
     return at(p, 16) && (rows <= 1 || (stride % 8 == 0 && stride >= cols && stride < (1ll << 36)));
 }
 
-// Workspace, in 256-byte regions: status word | x, Wg, Wu brought to 16-byte boundaries (calls with `copies`) | backward:
+// Workspace, in 256-byte regions: status | x, Wg, Wu brought to 16-byte boundaries (calls with `copies`) | backward:
 // dg, du | partial results.
 struct Layout {
     size_t x, wg, wu, dg, du, part, total;
@@ -126,7 +126,7 @@ gdr_status gdr_ffn_fwd(const gdr_ffn_fwd_args *a, void *stream_) {
         return GDR_ERR_INVALID_ARG;
     char *ws = (char *)a->workspace;
     FfnPad pad = {};
-    pad.status = (int *)ws;
+    pad.status = (uint8_t *)ws;
     to_rows(pad, x, ws + l.x, a->tokens, a->dim);
     to_rows(pad, wg, ws + l.wg, a->inner, a->dim);
     to_rows(pad, wu, ws + l.wu, a->inner, a->dim);
@@ -139,7 +139,7 @@ gdr_status gdr_ffn_fwd(const gdr_ffn_fwd_args *a, void *stream_) {
     FfnGemm p = {};
     p.job[0] = job_of(FFN_FWD, l.forward, a->h, nullptr, a->tokens, a->inner);
     p.gate = a->gate, p.up = a->up, p.piece32 = piece_of(a->gate, a->up, a->inner * 4), p.part = (float *)(ws + l.part);
-    p.dtype = a->dtype, p.act = a->activation, p.spin = spin_limit(), p.status = (int *)ws, p.clear = ws && pad.count == 0;
+    p.dtype = a->dtype, p.act = a->activation, p.spin = spin_limit(), p.status = (uint8_t *)ws, p.clear = ws && pad.count == 0;
     return done(launch_ffn_product(maps, p, stream));
 }
 
@@ -177,10 +177,10 @@ gdr_status gdr_ffn_bwd(const gdr_ffn_bwd_args *a, void *stream_) {
     FfnAct act = {};
     act.dh = a->dh, act.gate = a->gate, act.up = a->up, act.dg = ws + l.dg, act.du = ws + l.du;
     act.dh_ts = a->dh_token_stride, act.tokens = a->tokens, act.inner = a->inner, act.pitch = round8(a->inner);
-    act.dtype = a->dtype, act.act = a->activation, act.vec = v.ok, act.status = (int *)ws;
+    act.dtype = a->dtype, act.act = a->activation, act.vec = v.ok, act.status = (uint8_t *)ws;
     cudaError_t e = launch_ffn_act(act, stream);
     FfnPad pad = {};
-    pad.status = (int *)ws;
+    pad.status = (uint8_t *)ws;
     if (a->dx) to_rows(pad, wg, ws + l.wg, a->inner, a->dim), to_rows(pad, wu, ws + l.wu, a->inner, a->dim);
     if (a->dw_gate) to_rows(pad, x, ws + l.x, a->tokens, a->dim);
     if (e == cudaSuccess && pad.count) e = launch_ffn_pad(pad, stream);
@@ -188,7 +188,7 @@ gdr_status gdr_ffn_bwd(const gdr_ffn_bwd_args *a, void *stream_) {
     const Rows d[2] = {{act.dg, act.pitch}, {act.du, act.pitch}};
     FfnMaps maps;
     FfnGemm p = {};
-    p.part = (float *)(ws + l.part), p.dtype = a->dtype, p.spin = spin_limit(), p.status = (int *)ws;
+    p.part = (float *)(ws + l.part), p.dtype = a->dtype, p.spin = spin_limit(), p.status = (uint8_t *)ws;
     int jobs = 0;
     for (int j = 0; j < 2; ++j) {
         const bool dx = (j == 0) != l.backward.swapped;
@@ -209,6 +209,17 @@ gdr_status gdr_ffn_bwd(const gdr_ffn_bwd_args *a, void *stream_) {
     return done(e);
 }
 
-gdr_status gdr_ffn_get_status(void *workspace, void *stream) { return gdr_linrec_get_status(workspace, stream); }
+gdr_status gdr_ffn_get_status(void *workspace, void *stream_) {
+    if (!workspace || !at(workspace, 256)) return GDR_ERR_INVALID_ARG;
+    cudaStream_t stream = (cudaStream_t)stream_;
+    uint8_t status[GDR_FFN_STATUS_BYTES] = {};
+    // all of it on the caller's stream, and done on return: the workspace may be given away then
+    if (cudaMemcpyAsync(status, workspace, sizeof(status), cudaMemcpyDeviceToHost, stream) != cudaSuccess) return GDR_ERR_CUDA;
+    if (cudaMemsetAsync(workspace, 0, sizeof(status), stream) != cudaSuccess) return GDR_ERR_CUDA;
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return GDR_ERR_CUDA;
+    for (const uint8_t ran_out : status)
+        if (ran_out) return GDR_ERR_TIMEOUT;
+    return GDR_OK;
+}
 
 }  // extern "C"

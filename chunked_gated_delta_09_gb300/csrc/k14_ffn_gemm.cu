@@ -310,7 +310,6 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) k14_gemm(const __grid_constan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? pair_rank() : 0;
     if (threadIdx.x == 0) {
-        if (p.clear && blockIdx.x == 0) *p.status = 0;
         for (int s = 0; s < STAGES; ++s) tc::mbar_init(&full[s], 1), tc::mbar_init(&empty[s], 1);
         for (int b = 0; b < 2; ++b) tc::mbar_init(&done[b], 1), tc::mbar_init(&taken[b], STORE_WARPS * (PAIR ? 2 : 1));
         tc::mbar_init(&last, 1);
@@ -378,8 +377,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) k14_gemm(const __grid_constan
             }
         }
     }
-    if (lost && p.status) atomicOr(p.status, ST_TIMEOUT);
-    __syncthreads();
+    __syncwarp();
+    const int any = __syncthreads_or(lost);
+    if (threadIdx.x == 0 && p.status) {
+        p.status[blockIdx.x] = (uint8_t)(any || (!p.clear && p.status[blockIdx.x]));
+        if (p.clear)  // (those of CTAs that an earlier call had more of)
+            for (uint32_t i = blockIdx.x + gridDim.x; i < GDR_FFN_STATUS_BYTES; i += gridDim.x) p.status[i] = 0;
+    }
     __syncwarp();
     if (PAIR) pair_sync();
     if (threadIdx.x == 0 && rank == 0) {
@@ -410,7 +414,8 @@ template <bool FWD, int ACT, bool PAIR, typename T> cudaError_t gemm_t(const Ffn
     cudaError_t e = device_sm_count(&sms);
     if (e == cudaSuccess) e = smem_opt_in((const void *)k14_gemm<FWD, ACT, PAIR, T>, gemm_smem(PAIR));
     if (e != cudaSuccess) return e;
-    const int units = p.job[0].plan.units() + p.job[1].plan.units(), ctas = PAIR ? 2 : 1, most = sms / ctas;
+    const int units = p.job[0].plan.units() + p.job[1].plan.units(), ctas = PAIR ? 2 : 1;
+    const int most = min(sms, GDR_FFN_STATUS_BYTES) / ctas;  // (a byte of the status for each)
     ClusterLaunch l((units < most ? units : most) * ctas, GEMM_THREADS, gemm_smem(PAIR), ctas, stream);
     return cudaLaunchKernelEx(&l.cfg, k14_gemm<FWD, ACT, PAIR, T>, maps, p);
 }

@@ -133,9 +133,14 @@ template <int ACT, bool VEC, typename T> cudaError_t few_t(const FfnFew &p, cuda
 // ---------------------------------------------------------------- element-wise part of the backward pass
 constexpr int ROW_THREADS = 256;
 
+__device__ __forceinline__ void clear_status(uint8_t *status) {
+    static_assert(GDR_FFN_STATUS_BYTES <= ROW_THREADS);
+    if (blockIdx.x == 0 && threadIdx.x < GDR_FFN_STATUS_BYTES) status[threadIdx.x] = 0;
+}
+
 // Rows that are multiples of 16 bytes: 8 elements for each thread.  Others: 256 for each warp, its lanes side by side.
 template <int ACT, bool VEC, typename T> __global__ void __launch_bounds__(ROW_THREADS) k15_act(const FfnAct p, const FastDiv blocks) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+    clear_status(p.status);
     const T *dh = static_cast<const T *>(p.dh);
     T *dg = static_cast<T *>(p.dg), *du = static_cast<T *>(p.du);
     if constexpr (VEC) {
@@ -188,7 +193,7 @@ template <typename T> cudaError_t act_t(const FfnAct &p, cudaStream_t stream) {
 // ---------------------------------------------------------------- rows to 16-byte boundaries
 // 256 elements of a row for each warp, its lanes side by side.
 __global__ void __launch_bounds__(ROW_THREADS) k15_pad(const FfnPad p) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+    clear_status(p.status);
     uint32_t i = blockIdx.x * (ROW_THREADS / 32) + threadIdx.x / 32;
     int m = 0;
     while (m < p.count && i >= p.warps[m]) i -= p.warps[m++];

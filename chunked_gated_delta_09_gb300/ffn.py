@@ -38,12 +38,12 @@ def _check(x, w_gate, w_up, activation):
 
 
 def _workspace(x, xs, w_gate, w_up, strides, tokens, dim, inner, backward, status):
-    """(tensor or None, bytes) of a call's workspace, and whether it is to have a status word by all means."""
+    """(tensor or None, bytes) of a call's workspace, and whether it is to have a status by all means."""
     gs, us = strides
     copies = ((x.data_ptr() | w_gate.data_ptr() | w_up.data_ptr()) % 16 or (xs | gs | us) % 8
               or xs < dim or gs < dim or us < dim)
     nbytes = _entry("gdr_ffn_workspace_bytes")(tokens, dim, inner, 1 if copies else 0, backward)
-    if nbytes == 0 or (nbytes == _lib.FFN_STATUS_BYTES and not status):  # nothing but the status word
+    if nbytes == 0 or (nbytes == _lib.FFN_STATUS_BYTES and not status):  # nothing but the status
         return None, 0
     return x.new_empty(nbytes, dtype=torch.uint8), nbytes
 

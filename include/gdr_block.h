@@ -237,7 +237,7 @@ gdr_status gdr_load_states(const gdr_state_cache_args *args, void *stream);
  * formula, g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2.
  * gate, up fp32 [tokens, inner], both or neither (NULL): g and u for the backward.  h may be NULL with them.
  * workspace: gdr_ffn_workspace_bytes bytes, 256-byte aligned, not used by another call that may run at the same time; NULL
- * where that is 0, or GDR_FFN_STATUS_BYTES: the status word alone.  Waits that expire are read with gdr_ffn_get_status. */
+ * where that is 0, or GDR_FFN_STATUS_BYTES: the status alone.  Waits that expire are read with gdr_ffn_get_status. */
 #define GDR_FFN_MAX_DIM (1 << 20)
 /* Forward calls of up to so many tokens take no workspace. */
 #define GDR_FFN_FEW_TOKENS 32
@@ -272,7 +272,8 @@ gdr_status gdr_ffn_bwd(const gdr_ffn_bwd_args *args, void *stream);
  * start at multiples of 16 bytes (such are brought there first).  0 for bad sizes, and for forward calls of few tokens. */
 size_t gdr_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t inner, int copies, int backward);
 
-/* As gdr_linrec_get_status, for the last feed-forward call on this workspace. */
+/* Of the last feed-forward call on this workspace: synchronises `stream`, returns GDR_OK or GDR_ERR_TIMEOUT and clears the
+ * status, the workspace's first GDR_FFN_STATUS_BYTES. */
 gdr_status gdr_ffn_get_status(void *workspace, void *stream);
 
 #ifdef __cplusplus

@@ -317,3 +317,23 @@ def test_forward_mode_is_refused(which, grad):
         with pytest.raises(NotImplementedError):
             gated_ffn(*dual)
     assert torch.equal(gated_ffn(*parts), want)
+
+
+def test_every_cta_has_a_report_of_its_own(monkeypatch):
+    tokens, dim, inner = 640, 512, 512
+    x, wg, wu, _ = F.inputs(23, tokens, dim, inner, BF16)
+    h = torch.empty(tokens, inner, dtype=BF16, device="cuda")
+    lib, stream = _lib.load(), torch.cuda.current_stream().cuda_stream
+    n = lib.gdr_ffn_workspace_bytes(tokens, dim, inner, 0, 0)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    packed = _pack_fwd(x.data_ptr(), wg.data_ptr(), wu.data_ptr(), h.data_ptr(), 0, 0, ws.data_ptr(), tokens, dim, inner, dim, dim,
+                       dim, n, 1, 0)
+    status = ws[:_lib.FFN_STATUS_BYTES]
+    assert lib.gdr_ffn_fwd(packed, stream) == 0
+    assert not status.any()  # also what an earlier call of more CTAs would have left
+    monkeypatch.setenv("GDR_SPIN_LIMIT", "1")
+    assert lib.gdr_ffn_fwd(packed, stream) == 0
+    monkeypatch.delenv("GDR_SPIN_LIMIT")
+    assert int((status != 0).sum()) > 1
+    assert lib.gdr_ffn_get_status(ws.data_ptr(), stream) == _lib.GDR_ERR_TIMEOUT
+    assert lib.gdr_ffn_get_status(ws.data_ptr(), stream) == 0
