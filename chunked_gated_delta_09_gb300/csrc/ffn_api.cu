@@ -73,6 +73,12 @@ cudaError_t map_of(CUtensorMap &m, Rows r, int dtype, int64_t rows, int64_t cols
     return encode_matrix_map_sw128(&m, r.p, dtype, rows, cols, rows > 1 ? r.stride : round8(cols), box_rows);
 }
 
+// The status in the workspace of a call in which nothing waits, where it is given one.
+cudaError_t clear_status(void *ws, uint64_t bytes, cudaStream_t stream) {
+    if (!ws || !at(ws, 256) || bytes < GDR_FFN_STATUS_BYTES) return cudaSuccess;
+    return cudaMemsetAsync(ws, 0, GDR_FFN_STATUS_BYTES, stream);
+}
+
 int piece_of(const void *t, const void *u, int64_t row_bytes) {
     int n = 32;
     while (n > 8 && !(at(t, n) && at(u, n) && row_bytes % n == 0)) n /= 2;
@@ -100,7 +106,7 @@ gdr_status gdr_ffn_fwd(const gdr_ffn_fwd_args *a, void *stream_) {
     if ((a->dtype != GDR_BF16 && a->dtype != GDR_F16) || a->activation < 0 || a->activation > GDR_FFN_GELU_TANH ||
         !a->gate != !a->up || (!a->h && !a->gate))
         return a->dtype == GDR_F32 ? GDR_ERR_UNSUPPORTED : GDR_ERR_INVALID_ARG;
-    if (a->tokens == 0) return GDR_OK;
+    if (a->tokens == 0) return done(clear_status(a->workspace, a->workspace_bytes, stream));
     if (!a->x || !a->w_gate || !a->w_up || a->x_token_stride < 0 || a->w_gate_row_stride < 0 || a->w_up_row_stride < 0)
         return GDR_ERR_INVALID_ARG;
     if (!at(a->x, 2) || !at(a->w_gate, 2) || !at(a->w_up, 2) || !at(a->h, 2) || !at(a->gate, 4) || !at(a->up, 4))
@@ -115,7 +121,8 @@ gdr_status gdr_ffn_fwd(const gdr_ffn_fwd_args *a, void *stream_) {
         p.x_ts = a->x_token_stride, p.wg_rs = a->w_gate_row_stride, p.wu_rs = a->w_up_row_stride;
         p.tokens = (int)a->tokens, p.dim = (int)a->dim, p.inner = (int)a->inner, p.dtype = a->dtype, p.act = a->activation;
         p.vec = v.ok;
-        return done(launch_ffn_few(p, stream));
+        const cudaError_t e = clear_status(a->workspace, a->workspace_bytes, stream);
+        return done(e != cudaSuccess ? e : launch_ffn_few(p, stream));
     }
     Rows x = {a->x, a->x_token_stride}, wg = {a->w_gate, a->w_gate_row_stride}, wu = {a->w_up, a->w_up_row_stride};
     const bool copies = !mappable(x.p, x.stride, a->tokens, a->dim) || !mappable(wg.p, wg.stride, a->inner, a->dim) ||
@@ -152,13 +159,13 @@ gdr_status gdr_ffn_bwd(const gdr_ffn_bwd_args *a, void *stream_) {
         !a->dw_gate != !a->dw_up)
         return a->dtype == GDR_F32 ? GDR_ERR_UNSUPPORTED : GDR_ERR_INVALID_ARG;
     if (!at(a->dx, 2) || !at(a->dw_gate, 2) || !at(a->dw_up, 2)) return GDR_ERR_INVALID_ARG;
-    if (a->tokens == 0) {
-        if (!a->dw_gate) return GDR_OK;
+    if (a->tokens == 0 || (!a->dx && !a->dw_gate)) {
         const size_t bytes = (size_t)(a->inner * a->dim) * 2;
-        const cudaError_t e = cudaMemsetAsync(a->dw_gate, 0, bytes, stream);
-        return done(e != cudaSuccess ? e : cudaMemsetAsync(a->dw_up, 0, bytes, stream));
+        cudaError_t e = clear_status(a->workspace, a->workspace_bytes, stream);
+        if (e == cudaSuccess && a->dw_gate) e = cudaMemsetAsync(a->dw_gate, 0, bytes, stream);
+        if (e == cudaSuccess && a->dw_gate) e = cudaMemsetAsync(a->dw_up, 0, bytes, stream);
+        return done(e);
     }
-    if (!a->dx && !a->dw_gate) return GDR_OK;
     if (!a->dh || !a->gate || !a->up || (a->dw_gate && !a->x) || (a->dx && (!a->w_gate || !a->w_up)) || a->dh_token_stride < 0 ||
         a->x_token_stride < 0 || a->w_gate_row_stride < 0 || a->w_up_row_stride < 0)
         return GDR_ERR_INVALID_ARG;

@@ -237,7 +237,8 @@ gdr_status gdr_load_states(const gdr_state_cache_args *args, void *stream);
  * formula, g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2.
  * gate, up fp32 [tokens, inner], both or neither (NULL): g and u for the backward.  h may be NULL with them.
  * workspace: gdr_ffn_workspace_bytes bytes, 256-byte aligned, not used by another call that may run at the same time; NULL
- * where that is 0, or GDR_FFN_STATUS_BYTES: the status alone.  Waits that expire are read with gdr_ffn_get_status. */
+ * where that is 0, or GDR_FFN_STATUS_BYTES: the status alone.  Waits that expire are read with gdr_ffn_get_status; calls in which
+ * nothing waits (few tokens, none, or no result wanted) clear the status of a workspace that they are given all the same. */
 #define GDR_FFN_MAX_DIM (1 << 20)
 /* Forward calls of up to so many tokens take no workspace. */
 #define GDR_FFN_FEW_TOKENS 32

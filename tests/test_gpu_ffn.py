@@ -337,3 +337,32 @@ def test_every_cta_has_a_report_of_its_own(monkeypatch):
     assert int((status != 0).sum()) > 1
     assert lib.gdr_ffn_get_status(ws.data_ptr(), stream) == _lib.GDR_ERR_TIMEOUT
     assert lib.gdr_ffn_get_status(ws.data_ptr(), stream) == 0
+
+
+@pytest.mark.parametrize("call", ["few tokens", "no tokens", "no tokens backward", "nothing wanted"])
+def test_calls_that_wait_for_nothing_clear_the_status(monkeypatch, call):
+    tokens, dim, inner = 600, 64, 96
+    x, wg, wu, dh = F.inputs(22, tokens, dim, inner, BF16)
+    h = torch.empty_like(dh)
+    g, u = torch.zeros(2, tokens, inner, device="cuda")
+    lib, stream = _lib.load(), torch.cuda.current_stream().cuda_stream
+    n = lib.gdr_ffn_workspace_bytes(tokens, dim, inner, 0, 1)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    ptrs = [t.data_ptr() for t in (x, wg, wu)]
+
+    def fwd(count):
+        return lib.gdr_ffn_fwd(_pack_fwd(*ptrs, h.data_ptr(), 0, 0, ws.data_ptr(), count, dim, inner, dim, dim, dim, n, 1, 0), stream)
+
+    def bwd(count):
+        return lib.gdr_ffn_bwd(_pack_bwd(dh.data_ptr(), *ptrs, g.data_ptr(), u.data_ptr(), 0, 0, 0, ws.data_ptr(), count, dim,
+                                         inner, inner, dim, dim, dim, n, 1, 0), stream)
+
+    calls = {"few tokens": lambda: fwd(8), "no tokens": lambda: fwd(0), "no tokens backward": lambda: bwd(0),
+             "nothing wanted": lambda: bwd(tokens)}
+    monkeypatch.setenv("GDR_SPIN_LIMIT", "1")
+    assert fwd(tokens) == 0
+    assert lib.gdr_ffn_get_status(ws.data_ptr(), stream) == _lib.GDR_ERR_TIMEOUT
+    assert fwd(tokens) == 0
+    monkeypatch.delenv("GDR_SPIN_LIMIT")
+    assert calls[call]() == 0
+    assert lib.gdr_ffn_get_status(ws.data_ptr(), stream) == 0
