@@ -10,7 +10,8 @@
 // formed once for all rows.  Decays are multiplied, never divided: a gate of -inf forgets and nothing else.
 //
 // A CTA has up to `rows` rows of one state, which come by asynchronous copies into shared memory while the vectors are formed.
-// One token reads and writes each state once, 8 bytes for 8 operations: HBM bounds it (256 x 32 states: 159 us, 6.65 TB/s).
+// One token reads and writes each state once, 8 bytes for 8 operations: HBM bounds it (251 x 32 states of
+// 128 x 128: 159 us, 6.68 TB/s).
 #include "block_common.cuh"
 #include "delta_step.h"
 #include "tc_util.cuh"
@@ -460,10 +461,16 @@ template <typename T, int CH> cudaError_t few_of(const RuleStepParams &p, cudaSt
     return p.T <= 3 ? few_t<T, 3, CH>(p, stream) : p.T <= 5 ? few_t<T, 5, CH>(p, stream) : few_t<T, 8, CH>(p, stream);
 }
 template <typename T> cudaError_t step_of(RuleStepParams p, cudaStream_t stream) {
-    // Tokens in turn, or all products with the state as it was read, by whichever is quicker (256 x 32 states of 128 x 128, us in
-    // turn and together; states moved: 2 tokens 163 and 238, 4 217 and 251, 5 245 and 252, 6 292 and 272; outputs alone:
-    // 2 tokens 117 and 134, 3 145 and 136).  In turn, 64 rows to a CTA (one token: 164 us, 174 with 128, 186 with 32); together,
-    // all of them, since each CTA forms the vectors again.
+    // Tokens in turn, or all products with the state as it was read.  us in turn and together, 256 x 32 states of 128 x 128, 64 x 64
+    // and 32 x 32:
+    //     states moved   2 tokens  167, 238   50, 72   27, 29        outputs alone   2 tokens  131, 134   43, 54   26, 25
+    //                    4         238, 250   74, 78   38, 33                        3         164, 135   54, 54   30, 25
+    //                    5         271, 252   84, 79   42, 33                        5         248, 150   80, 61   41, 29
+    // So moved states go in turn up to 4 tokens where rows are long, and outputs alone up to 2; the fifth token, and the fourth of
+    // states of 32 x 32, cost up to 27 % more in turn, but stay in fp32.  16 x 32 states of 128 x 128: 14 and 19 for 2 tokens
+    // that move them, 20 and 20 for 4, 22 and 20 for 5.
+    // In turn, 64 rows to a CTA (one token: 158 us, 160 with 128, 176 with 32; of 16 x 32 states 11.6, 14.6, 11.6); together, all
+    // of them, since each CTA forms the vectors again.
     const bool turn = p.T <= (p.update ? 5 : 2);
     p.rows = turn && p.V > 64 ? 64 : p.V;
     if (turn) return p.K <= 32 ? turn_of<T, 1>(p, stream) : p.K <= 64 ? turn_of<T, 2>(p, stream) : turn_of<T, 4>(p, stream);

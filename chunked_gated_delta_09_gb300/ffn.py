@@ -87,7 +87,8 @@ def gated_ffn_bwd(dh, x, w_gate, w_up, saved=None, *, activation="silu", need_dx
     ``need_dx`` and ``need_dw`` leave out.
 
     dh like h; saved as ``return_saved`` gave it on the same x and weights, or None: the projections are computed first, by
-    one more forward pass.  The gradients of the two projections are rounded to x's type before the products with them."""
+    one more forward pass, which ``check_status`` covers too.  The gradients of the two projections are rounded to x's type
+    before the products with them: in fp16 they have its range (infinite past 65504, 0 below 2^-25), so scale the loss for it."""
     if stream is not None:
         with _on(stream, (dh, x, w_gate, w_up, saved)):
             return gated_ffn_bwd(dh, x, w_gate, w_up, saved, activation=activation, need_dx=need_dx, need_dw=need_dw,

@@ -238,7 +238,8 @@ gdr_status gdr_load_states(const gdr_state_cache_args *args, void *stream);
  * gate, up fp32 [tokens, inner], both or neither (NULL): g and u for the backward.  h may be NULL with them.
  * workspace: gdr_ffn_workspace_bytes bytes, 256-byte aligned, not used by another call that may run at the same time; NULL
  * where that is 0, or GDR_FFN_STATUS_BYTES: the status alone.  Waits that expire are read with gdr_ffn_get_status; calls in which
- * nothing waits (few tokens, none, or no result wanted) clear the status of a workspace that they are given all the same. */
+ * nothing waits (few tokens, none, or no result wanted) clear the status of a workspace
+ * of GDR_FFN_STATUS_BYTES or more that they are given all the same. */
 #define GDR_FFN_MAX_DIM (1 << 20)
 /* Forward calls of up to so many tokens take no workspace. */
 #define GDR_FFN_FEW_TOKENS 32
@@ -255,7 +256,7 @@ typedef struct {
 } gdr_ffn_fwd_args;
 gdr_status gdr_ffn_fwd(const gdr_ffn_fwd_args *args, void *stream);
 
-/* Gradients of sum(h * dh): with dg = dh u act'(g) and du = dh act(g), rounded to dtype,
+/* Gradients of sum(h * dh): with dg = dh u act'(g) and du = dh act(g), rounded to dtype (and within its range),
  *     dx = dg w_gate + du w_up [tokens, dim] ,   dw_gate = dg^T x ,  dw_up = du^T x [inner, dim]   (all in dtype)
  * gate and up are what the forward call wrote.  dx may be NULL (not returned, the weights are not read), and so may dw_gate
  * and dw_up together (x is not read). */
